@@ -12,6 +12,14 @@ Functions carry the C ABI's names (include/qlora_nf4.h):
     qlora_linear_fwd(w, x, A, B, alpha)       -> (Y, U)
     qlora_linear_bwd(w, x, dY, A, B, alpha, U=None, need_dx=True) -> (dX, dA, dB)
     qlora_nf4_codebook(), qlora_nf4_thresholds()   (host only, no GPU needed)
+
+and, around the linear layer in a fine-tuning step:
+
+    qlora_layernorm_fwd(x, weight, bias)      -> (y, mean, rstd)
+    qlora_layernorm_bwd(x, dy, mean, rstd, weight) -> (dx, dweight, dbias)
+    qlora_logprob_fwd(logits, targets, top)   -> (logp, entropy, lse, top_logp, top_ids)
+    qlora_logprob_bwd(logits, targets, lse, entropy, dlogp, dentropy) -> dlogits
+    qlora_adamw_step(AdamWPlan(params, grads, m, v, ...), lr=..., step=...)
 """
 from __future__ import annotations
 
@@ -28,6 +36,8 @@ BLOCK = 64
 DQ_BLOCK = 256
 NO_DQ = 0  # dq_block of the format without double quantization (fp32 absmax per block)
 C2_INT8, C2_FP8_E4M3 = 0, 1  # c2_format: how the c2 bytes of a double-quantized weight encode values
+STATE_BLOCK = 256  # elements that share the scales of 8-bit AdamW states
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # QLORA_BF16, QLORA_F32
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -43,6 +53,19 @@ class _CWeight(ctypes.Structure):
                 ("d", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("block", ctypes.c_int32), ("dq_block", ctypes.c_int32),
                 ("c2_format", ctypes.c_int32)]
+
+
+class _CAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class _CAdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("state_type", ctypes.c_int32), ("use_master", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -76,6 +99,16 @@ _SIGS = {
                                                 ctypes.c_uint64, _P, _P, _P, _SZ, _P]),
     "qlora_linear_bwd_dropout": (ctypes.c_int, [_WP, _P, _P, _P, _P, _P, _I64, _I32, ctypes.c_float,
                                                 ctypes.c_float, ctypes.c_uint64, _P, _P, _P, _P, _SZ, _P]),
+    "qlora_layernorm_fwd": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _P]),
+    "qlora_layernorm_workspace": (_SZ, [_I64, _I64]),
+    "qlora_layernorm_bwd": (ctypes.c_int, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _P, _SZ,
+                                           _P]),
+    "qlora_logprob_workspace": (_SZ, [_I64, _I64, _I32]),
+    "qlora_logprob_fwd": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "qlora_logprob_bwd": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "qlora_adamw_step": (ctypes.c_int, [ctypes.POINTER(_CAdamWTensor), _I32, ctypes.POINTER(_CAdamWConfig), _P]),
+    "qlora_adamw_moments": (ctypes.c_int, [ctypes.POINTER(_CAdamWTensor), _I32, ctypes.POINTER(_P),
+                                           ctypes.POINTER(_P), _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     if not hasattr(_lib, _name):
@@ -396,7 +429,214 @@ def qlora_adapter_unmerge(w_in: torch.Tensor, a: torch.Tensor, b: torch.Tensor, 
     return y
 
 
+def _element_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The row pitch, in elements, of a device matrix whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with dense rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shaped(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> torch.Tensor:
+    _dev_tensor(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def qlora_layernorm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                        eps: float = 1e-5, out: torch.Tensor | None = None, save_stats: bool = True):
+    """y = (x - mean) rstd weight + bias over the rows of x [M, n] (bf16 or fp32, rows at any pitch).
+    Returns (y like x, mean fp32 [M], rstd fp32 [M]), the statistics None without save_stats."""
+    kind, ld = _element_type(x, "x"), _rows(x, "x")
+    m, n = x.shape
+    ref = weight if weight is not None else bias
+    wkind = _element_type(ref, "weight") if ref is not None else 0
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _shaped(t, ref.dtype, (n,), name)
+    y = _shaped(out, x.dtype, (m, n), "out") if out is not None else torch.empty((m, n), dtype=x.dtype, device=x.device)
+    mean = torch.empty(m, dtype=torch.float32, device=x.device) if save_stats else None
+    rstd = torch.empty(m, dtype=torch.float32, device=x.device) if save_stats else None
+    _check(_lib.qlora_layernorm_fwd(x.data_ptr(), kind, m, n, ld, _ptr(weight), _ptr(bias), wkind, float(eps),
+                                    y.data_ptr(), _ptr(mean), _ptr(rstd), _stream()), "qlora_layernorm_fwd")
+    return y, mean, rstd
+
+
+def qlora_layernorm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, need_dw: bool = True, need_db: bool = True,
+                        workspace: torch.Tensor | None = None, outs: tuple | None = None):
+    """Returns (dx like dy, dweight fp32 [n] or None, dbias fp32 [n] or None); mean and rstd are the
+    forward's.  outs: the three of them, None in place of a gradient that is not wanted."""
+    kind, ld = _element_type(x, "x"), _rows(x, "x")
+    m, n = x.shape
+    _shaped(dy, x.dtype, (m, n), "dy")
+    _shaped(mean, torch.float32, (m,), "mean")
+    _shaped(rstd, torch.float32, (m,), "rstd")
+    wkind = 0
+    if weight is not None:
+        wkind = _element_type(weight, "weight")
+        _shaped(weight, weight.dtype, (n,), "weight")
+    if outs is not None:
+        dx, dw, db = outs
+        _shaped(dx, x.dtype, (m, n), "dx")
+        for t, name in ((dw, "dweight"), (db, "dbias")):
+            if t is not None:
+                _shaped(t, torch.float32, (n,), name)
+    else:
+        dx = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        dw = torch.empty(n, dtype=torch.float32, device=x.device) if need_dw else None
+        db = torch.empty(n, dtype=torch.float32, device=x.device) if need_db else None
+    ws = workspace
+    if ws is None and (dw is not None or db is not None):
+        ws = _workspace(layernorm_workspace_bytes(m, n), x.device)
+    _check(_lib.qlora_layernorm_bwd(x.data_ptr(), dy.data_ptr(), kind, m, n, ld, mean.data_ptr(), rstd.data_ptr(),
+                                    _ptr(weight), wkind, dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws),
+                                    ws.numel() if ws is not None else 0, _stream()), "qlora_layernorm_bwd")
+    return dx, dw, db
+
+
+def layernorm_workspace_bytes(m: int, n: int) -> int:
+    return int(_lib.qlora_layernorm_workspace(m, n))
+
+
+def logprob_workspace_bytes(m: int, v: int, top: int = 0) -> int:
+    return int(_lib.qlora_logprob_workspace(m, v, top))
+
+
+def qlora_logprob_fwd(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
+                      workspace: torch.Tensor | None = None):
+    """Log-probabilities of the targets (int64 [M]; outside [0, V): no target, 0) under logits [M, V]
+    (bf16 or fp32, rows at any pitch, -inf for tokens that are ruled out).  Returns fp32 [M] logp, entropy
+    and lse, and the `top` best alternatives: fp32 [M, top] log-probabilities and int32 [M, top] ids
+    (None, None with top = 0)."""
+    kind, ld = _element_type(logits, "logits"), _rows(logits, "logits")
+    m, v = logits.shape
+    _shaped(targets, torch.int64, (m,), "targets")
+    logp, entropy, lse = (torch.empty(m, dtype=torch.float32, device=logits.device) for _ in range(3))
+    top_logp = torch.empty((m, top), dtype=torch.float32, device=logits.device) if top > 0 else None
+    top_ids = torch.empty((m, top), dtype=torch.int32, device=logits.device) if top > 0 else None
+    ws = workspace if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), logits.device)
+    _check(_lib.qlora_logprob_fwd(logits.data_ptr(), kind, m, v, ld, targets.data_ptr(), int(top), logp.data_ptr(),
+                                  entropy.data_ptr(), lse.data_ptr(), _ptr(top_logp), _ptr(top_ids), ws.data_ptr(),
+                                  ws.numel(), _stream()), "qlora_logprob_fwd")
+    return logp, entropy, lse, top_logp, top_ids
+
+
+def qlora_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor | None,
+                      dlogp: torch.Tensor, dentropy: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits [M, V] (like logits) from the gradients of logp and, if given, entropy; out may be the
+    logits themselves (in place)."""
+    kind, ld = _element_type(logits, "logits"), _rows(logits, "logits")
+    m, v = logits.shape
+    _shaped(targets, torch.int64, (m,), "targets")
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        if t is not None:
+            _shaped(t, torch.float32, (m,), name)
+    if out is None:
+        out = torch.empty((m, v), dtype=logits.dtype, device=logits.device)
+    elif out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must have the logits' type and shape")
+    _check(_lib.qlora_logprob_bwd(logits.data_ptr(), kind, m, v, ld, targets.data_ptr(), _ptr(lse), _ptr(entropy),
+                                  _ptr(dlogp), _ptr(dentropy), out.data_ptr(), _rows(out, "out"), _stream()),
+           "qlora_logprob_bwd")
+    return out
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked and laid out once: params (bf16 or fp32), grads (bf16 or
+    fp32) and states of the same sizes.  States are fp32 m and v, or int8 m and uint8 v with fp32
+    scales (one for each 256 elements, the last block possibly shorter); masters are fp32 weights
+    beside bf16 params.  The plan keeps the tensors: every step reads and updates these buffers, so
+    gradients have to arrive in the same ones (qlora_linear_bwd's outs)."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, masters=None):
+        params, grads, m, v = list(params), list(grads), list(m), list(v)
+        count = len(params)
+        if not count:
+            raise ValueError("an AdamW plan needs at least one tensor")
+        self.bits8 = m_scales is not None
+        if self.bits8 != (v_scales is not None):
+            raise ValueError("8-bit states need m_scales and v_scales")
+        none = [None] * count
+        m_scales, v_scales = (list(m_scales), list(v_scales)) if self.bits8 else (none, none)
+        self.master = masters is not None
+        masters = list(masters) if self.master else none
+        for name, ts in (("grads", grads), ("m", m), ("v", v), ("m_scales", m_scales), ("v_scales", v_scales),
+                         ("masters", masters)):
+            if len(ts) != count:
+                raise ValueError(f"{count} params and {len(ts)} {name}")
+        self.param_type = _element_type(params[0], "params")
+        self.grad_type = _element_type(grads[0], "grads")
+        f32 = torch.float32
+        mt, vt = (torch.int8, torch.uint8) if self.bits8 else (f32, f32)
+        self.count = count
+        self.table = (_CAdamWTensor * count)()
+        self.tensors = (params, grads, m, v, m_scales, v_scales, masters)
+        for i, (p, g, mi, vi, ms, vs, w) in enumerate(zip(*self.tensors)):
+            n = p.numel()
+            for t, dtype, size, name in ((p, params[0].dtype, n, "params"), (g, grads[0].dtype, n, "grads"),
+                                         (mi, mt, n, "m"), (vi, vt, n, "v"), (ms, f32, -(-n // STATE_BLOCK), "m_scales"),
+                                         (vs, f32, -(-n // STATE_BLOCK), "v_scales"), (w, f32, n, "masters")):
+                if t is None and name not in ("params", "grads", "m", "v"):
+                    continue
+                if _dev_tensor(t, dtype, f"{name}[{i}]").numel() != size:
+                    raise ValueError(f"{name}[{i}] must have {size} elements, got {t.numel()}")
+            self.table[i] = _CAdamWTensor(_ptr(p), _ptr(g), _ptr(mi), _ptr(vi), _ptr(ms), _ptr(vs), _ptr(w), n)
+
+    @staticmethod
+    def zeros(params, grads, bits8: bool = True, master: bool = False) -> "AdamWPlan":
+        """A plan with new states (zeros) for params, and with `master` fp32 copies of them."""
+        params = list(params)
+        mt, vt = (torch.int8, torch.uint8) if bits8 else (torch.float32, torch.float32)
+        scales = (lambda: [torch.zeros(-(-p.numel() // STATE_BLOCK), dtype=torch.float32, device=p.device)
+                           for p in params]) if bits8 else (lambda: None)
+        return AdamWPlan(params, grads, [torch.zeros(p.shape, dtype=mt, device=p.device) for p in params],
+                         [torch.zeros(p.shape, dtype=vt, device=p.device) for p in params], scales(), scales(),
+                         [p.float() for p in params] if master else None)
+
+
+def qlora_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999,
+                     eps: float = 1e-8, weight_decay: float = 0.0, grad_scale: float = 1.0) -> None:
+    """One AdamW step on the plan's tensors, on the current stream; `step` counts from 1."""
+    config = _CAdamWConfig(lr, beta1, beta2, eps, weight_decay, grad_scale, step, plan.param_type, plan.grad_type,
+                           int(plan.bits8), int(plan.master))
+    _check(_lib.qlora_adamw_step(plan.table, plan.count, ctypes.byref(config), _stream()), "qlora_adamw_step")
+
+
+def qlora_adamw_moments(plan: AdamWPlan, m_out=None, v_out=None):
+    """The fp32 values of the plan's 8-bit states: (list of m, list of v)."""
+    if not plan.bits8:
+        raise ValueError("the plan's states are not in 8 bits")
+    outs = []
+    for given, name in ((m_out, "m_out"), (v_out, "v_out")):
+        ts = list(given) if given is not None else [torch.empty(t.shape, dtype=torch.float32, device=t.device)
+                                                     for t in plan.tensors[2]]
+        if len(ts) != plan.count:
+            raise ValueError(f"{plan.count} tensors and {len(ts)} {name}")
+        for i, (t, c) in enumerate(zip(ts, plan.tensors[2])):
+            if _dev_tensor(t, torch.float32, f"{name}[{i}]").numel() != c.numel():
+                raise ValueError(f"{name}[{i}] must have {c.numel()} elements")
+        outs.append(ts)
+    ptrs = [(_P * plan.count)(*[t.data_ptr() for t in ts]) for ts in outs]
+    _check(_lib.qlora_adamw_moments(plan.table, plan.count, ptrs[0], ptrs[1], _stream()), "qlora_adamw_moments")
+    return outs[0], outs[1]
+
+
 __all__ = [
+    "qlora_layernorm_fwd", "qlora_layernorm_bwd", "layernorm_workspace_bytes",
+    "qlora_logprob_fwd", "qlora_logprob_bwd", "logprob_workspace_bytes",
+    "AdamWPlan", "qlora_adamw_step", "qlora_adamw_moments", "STATE_BLOCK",
     "NF4Weight", "QloraError", "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",
     "qlora_linear_fwd_noalloc",
     "qlora_linear_bwd", "qlora_linear_gemm_only", "qlora_time_next_kernel", "wall_clock_khz",

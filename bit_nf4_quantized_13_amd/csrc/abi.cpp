@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "abi_util.hpp"
 #include "launch.hpp"
 
 using namespace qnf4;
@@ -17,10 +18,6 @@ constexpr int64_t kMaxWeights = int64_t(1) << 30;  // 2^24 NF4 blocks: 65536 DQ 
 constexpr int64_t kDecodeMaxK = int64_t(1) << 25;  // 32-bit buffer offsets of X and A rows
 constexpr int64_t kMaxDim = int64_t(1) << 20;      // d, k of a linear call: 32-bit offsets in GEMM tiles
 constexpr int64_t kMaxPlanes = int64_t(1) << 29;   // M * r16: U and G as transposed bf16 hi / lo planes
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Shape and format checks shared by every call that takes a weight.
 int check_weight(const qlora_nf4_weight *w, bool need_data) {
@@ -49,8 +46,6 @@ Nf4Weights nf4_view(const qlora_nf4_weight *w) {
     return Nf4Weights{w->codes, dq ? w->absmax_q : nullptr, w->absmax_scale, dq ? w->absmax_mean : nullptr,
                       w->d, w->k, fmt, bshift};
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_EHIP; }
 
 // ---- workspace layouts ------------------------------------------------------
 struct QuantWs {

@@ -1,0 +1,239 @@
+// One AdamW step over a list of tensors, element by element:
+//   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) (1 - b2^t)^-1/2 + eps)
+// with g the stored gradient times grad_scale.  Everything is fp32 between the
+// load and the store; a bf16 p (without a master) is rounded to nearest even.
+//
+// States in 8 bits, in blocks of 256 elements with one fp32 scale s each:
+//   m = sign(c) c^2 s   s = fp32(max|m| fp32(127^-2))   c = rint(sqrt(fp32(|m| fp32(1/s)))), |c| <= 127
+//   v = c^4 s           s = fp32(max v fp32(255^-4))    c = rint(sqrt(sqrt(fp32(v fp32(1/s))))), c >= 1 where v > 0
+// (c^2, c^4 in fp32 as (c c) (c c)).  The square and the fourth power spend the
+// codes evenly over the roots: the steps shrink with the value, v spans 9
+// decades, and sqrt(v), which divides, has the resolution of m.  v > 0 never
+// becomes 0, so m is never divided by eps alone.  A block whose scale would be
+// below the smallest normal number is stored as zeros.  All of it is fixed
+// IEEE arithmetic: the codes are reproducible bit for bit.
+//
+// Bound: HBM, 24 bytes an element with fp32 states, 12 with 8-bit states (bf16
+// p, fp32 g).  Each thread takes 8 consecutive elements of every array (16-byte
+// accesses), a block of 256 is half a wave, its maxima 5 lane exchanges.
+// Tensors go to the kernel as arguments, up to kMaxTensors a launch: nothing
+// about them is kept anywhere between calls.
+#include "elem8.hpp"
+#include "launch.hpp"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kMaxTensors = 48;        // 48 x 64 bytes of kernel arguments, of 4 KiB
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads * 8;   // elements a workgroup takes
+
+struct TensorList {
+    AdamwTensor t[kMaxTensors];
+    uint32_t first[kMaxTensors + 1];  // the tensors' first workgroups
+    int count;
+};
+
+constexpr float kMUnit = 1.0f / 16129.0f;       // 127^-2
+constexpr float kVUnit = 1.0f / 4228250625.0f;  // 255^-4, from 255^4 rounded to fp32
+
+// The tensor that a workgroup belongs to (first is ascending).
+__device__ __forceinline__ int tensor_of(const TensorList &list, uint32_t wg) {
+    int lo = 0, hi = list.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (list.first[mid] <= wg) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+struct U8x8 {
+    uint32_t w[2];
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+__device__ __forceinline__ U8x8 load_codes(const uint8_t *p, int64_t cnt) {
+    U8x8 r;
+    if (cnt >= 8) {
+        const u32x2 w = *reinterpret_cast<const u32x2_any *>(p);
+        r.w[0] = w.x;
+        r.w[1] = w.y;
+        return r;
+    }
+    r.w[0] = r.w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < cnt) r.w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    return r;
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, int64_t cnt, const U8x8 &r) {
+    if (cnt >= 8) {
+        *reinterpret_cast<u32x2_any *>(p) = u32x2{r.w[0], r.w[1]};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < cnt) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+}
+
+__device__ __forceinline__ float decode_m(const U8x8 &r, int i, float scale) {
+    const float c = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+    return c * fabsf(c) * scale;
+}
+__device__ __forceinline__ float decode_v(const U8x8 &r, int i, float scale) {
+    const float c = (float)(uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
+    return c * c * (c * c) * scale;
+}
+
+// Maximum over the half wave that holds a block.
+__device__ __forceinline__ float block_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ float block_scale_of(float top, float unit) {
+    const float s = top * unit;
+    return s >= 1.17549435e-38f ? s : 0.0f;
+}
+
+template <bool PF32, bool GF32, bool BITS8, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(TensorList list, AdamwHyper h) {
+    using P = std::conditional_t<PF32, float, uint16_t>;
+    using G = std::conditional_t<GF32, float, uint16_t>;
+    const int k = tensor_of(list, blockIdx.x);
+    const AdamwTensor &t = list.t[k];
+    const int64_t at = (int64_t)(blockIdx.x - list.first[k]) * kChunk + threadIdx.x * 8;
+    const int64_t cnt = t.n - at;  // may be <= 0: such lanes hold zeros
+    P *p = (P *)t.param + at;
+    float *master = MASTER ? t.master + at : nullptr;
+    F8 g = load8((const G *)t.grad + at, cnt), m, v;
+    F8 w = MASTER ? load8((const float *)master, cnt) : load8((const P *)p, cnt);
+    U8x8 mc, vc;
+    if (BITS8) {
+        mc = load_codes((const uint8_t *)t.m + at, cnt);
+        vc = load_codes((const uint8_t *)t.v + at, cnt);
+        const float ms = cnt > 0 ? t.m_scale[at >> 8] : 0.0f, vs = cnt > 0 ? t.v_scale[at >> 8] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m.v[i] = decode_m(mc, i, ms);
+            v.v[i] = decode_v(vc, i, vs);
+        }
+    } else {
+        m = load8((const float *)t.m + at, cnt);
+        v = load8((const float *)t.v + at, cnt);
+    }
+    float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float gi = g.v[i] * h.grad_scale;
+        m.v[i] = m.v[i] * h.beta1 + gi * h.one_minus_beta1;
+        v.v[i] = v.v[i] * h.beta2 + gi * gi * h.one_minus_beta2;
+        w.v[i] = w.v[i] * h.decay - h.step_size * (m.v[i] / (sqrtf(v.v[i]) * h.v_correction + h.eps));
+        if (BITS8) {
+            mtop = fmaxf(mtop, fabsf(m.v[i]));
+            vtop = fmaxf(vtop, v.v[i]);
+        }
+    }
+    if (MASTER) store8(master, cnt, w);
+    store8(p, cnt, w);
+    if (!BITS8) {
+        store8((float *)t.m + at, cnt, m);
+        store8((float *)t.v + at, cnt, v);
+        return;
+    }
+    const float ms = block_scale_of(block_max(mtop), kMUnit), vs = block_scale_of(block_max(vtop), kVUnit);
+    const float mi = ms > 0.0f ? 1.0f / ms : 0.0f, vi = vs > 0.0f ? 1.0f / vs : 0.0f;
+    mc.w[0] = mc.w[1] = vc.w[0] = vc.w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        int c = (int)fminf(rintf(sqrtf(fabsf(m.v[i]) * mi)), 127.0f);
+        c = m.v[i] < 0.0f ? -c : c;
+        mc.w[i >> 2] |= (uint32_t)(uint8_t)c << (8 * (i & 3));
+        int d = (int)fminf(rintf(sqrtf(sqrtf(v.v[i] * vi))), 255.0f);
+        if (v.v[i] > 0.0f && vs > 0.0f && d < 1) d = 1;
+        vc.w[i >> 2] |= (uint32_t)d << (8 * (i & 3));
+    }
+    store_codes((uint8_t *)t.m + at, cnt, mc);
+    store_codes((uint8_t *)t.v + at, cnt, vc);
+    if ((threadIdx.x & 31) == 0 && cnt > 0) {
+        t.m_scale[at >> 8] = ms;
+        t.v_scale[at >> 8] = vs;
+    }
+}
+
+// The values that 8-bit states stand for; here param and grad are the fp32
+// arrays that receive m and v.
+__global__ __launch_bounds__(kThreads) void adamw_moments_kernel(TensorList list) {
+    const int k = tensor_of(list, blockIdx.x);
+    const AdamwTensor &t = list.t[k];
+    const int64_t at = (int64_t)(blockIdx.x - list.first[k]) * kChunk + threadIdx.x * 8, cnt = t.n - at;
+    if (cnt <= 0) return;
+    const U8x8 mc = load_codes((const uint8_t *)t.m + at, cnt), vc = load_codes((const uint8_t *)t.v + at, cnt);
+    const float ms = t.m_scale[at >> 8], vs = t.v_scale[at >> 8];
+    F8 m, v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m.v[i] = decode_m(mc, i, ms);
+        v.v[i] = decode_v(vc, i, vs);
+    }
+    store8((float *)t.param + at, cnt, m);
+    store8((float *)const_cast<void *>(t.grad) + at, cnt, v);
+}
+
+// f(list, workgroups) for each launch's part of the tensors; empty ones are left out.
+template <typename F>
+hipError_t in_lists(const AdamwTensor *t, int count, F f) {
+    TensorList list;
+    list.count = 0;
+    uint32_t wgs = 0;
+    for (int i = 0; i <= count; ++i) {
+        const uint32_t need = i < count ? (uint32_t)((t[i].n + kChunk - 1) / kChunk) : 0;
+        if (list.count > 0 && (i == count || list.count == kMaxTensors || wgs + need > kMaxAdamwGroups)) {
+            list.first[list.count] = wgs;
+            f(list, wgs);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            list.count = 0;
+            wgs = 0;
+        }
+        if (need == 0) continue;
+        list.t[list.count] = t[i];
+        list.first[list.count++] = wgs;
+        wgs += need;
+    }
+    return hipSuccess;
+}
+
+template <bool PF32, bool GF32, bool BITS8, bool MASTER>
+hipError_t step(const AdamwTensor *t, int count, const AdamwHyper &h, hipStream_t s) {
+    return in_lists(t, count, [&](const TensorList &list, uint32_t wgs) {
+        adamw_kernel<PF32, GF32, BITS8, MASTER><<<wgs, kThreads, 0, s>>>(list, h);
+    });
+}
+
+template <bool PF32, bool MASTER>
+hipError_t step_typed(const AdamwTensor *t, int count, bool g_f32, bool bits8, const AdamwHyper &h, hipStream_t s) {
+    if (g_f32)
+        return bits8 ? step<PF32, true, true, MASTER>(t, count, h, s) : step<PF32, true, false, MASTER>(t, count, h, s);
+    return bits8 ? step<PF32, false, true, MASTER>(t, count, h, s) : step<PF32, false, false, MASTER>(t, count, h, s);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwTensor *t, int count, bool p_f32, bool g_f32, bool bits8, bool master,
+                        const AdamwHyper &h, hipStream_t s) {
+    if (p_f32) return step_typed<true, false>(t, count, g_f32, bits8, h, s);
+    return master ? step_typed<false, true>(t, count, g_f32, bits8, h, s)
+                  : step_typed<false, false>(t, count, g_f32, bits8, h, s);
+}
+
+hipError_t launch_adamw_moments(const AdamwTensor *t, int count, hipStream_t s) {
+    return in_lists(t, count, [&](const TensorList &list, uint32_t wgs) {
+        adamw_moments_kernel<<<wgs, kThreads, 0, s>>>(list);
+    });
+}
+
+}  // namespace qnf4

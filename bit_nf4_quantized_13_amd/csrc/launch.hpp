@@ -173,4 +173,53 @@ bool decode_dot_supported(int64_t M, int64_t d, int64_t k, int r);
 hipError_t launch_decode_dot(const Nf4Weights &w, const uint16_t *x, int64_t M, const uint16_t *A, const uint16_t *B,
                              int r, float s, uint16_t *Y, float *U_save, unsigned long long *span, hipStream_t st);
 
+// ---- layer norm (layernorm.hip) -----------------------------------------------
+// x, dy, y, dx of one type (fp32 or bf16), w and b of another or null; x's rows
+// ldx elements apart, the rest dense.  part: layernorm_part_bytes(M, n) bytes when
+// dw or db is given.
+size_t layernorm_part_bytes(int64_t M, int64_t n);
+hipError_t launch_layernorm_fwd(const void *x, bool x_f32, int64_t M, int64_t n, int64_t ldx, const void *w,
+                                const void *b, bool w_f32, float eps, void *y, float *mean, float *rstd,
+                                hipStream_t s);
+hipError_t launch_layernorm_bwd(const void *x, const void *dy, bool x_f32, int64_t M, int64_t n, int64_t ldx,
+                                const float *mean, const float *rstd, const void *w, bool w_f32, void *dx, float *dw,
+                                float *db, float *part, hipStream_t s);
+
+// ---- token log-probabilities (logprob.hip) --------------------------------------
+constexpr int kMaxTop = 16;                      // alternatives a row
+constexpr int64_t kMaxVocab = int64_t(1) << 19;  // 64 chunks of 8192: a lane each in the joining wave
+// A row's partial sums and best lists, and the workgroups the calls take.
+size_t logprob_stats_bytes(int64_t M, int64_t V);
+size_t logprob_best_bytes(int64_t M, int64_t V, int top);
+int64_t logprob_groups(int64_t M, int64_t V);
+hipError_t launch_logprob_fwd(const void *x, bool f32, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                              int top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
+                              float *stats, void *best, hipStream_t s);
+hipError_t launch_logprob_bwd(const void *x, bool f32, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                              const float *lse, const float *entropy, const float *dlogp, const float *dent, void *dx,
+                              int64_t ldd, hipStream_t s);
+
+// ---- AdamW (adamw.hip) -----------------------------------------------------------
+// One tensor of a step: the layout of qlora_adamw_tensor.
+struct AdamwTensor {
+    void *param;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    float *master;
+    int64_t n;
+};
+struct AdamwHyper {
+    float beta1, one_minus_beta1, beta2, one_minus_beta2;
+    float eps, decay, step_size, v_correction;  // 1 - lr wd, lr / (1 - b1^t), (1 - b2^t)^-1/2
+    float grad_scale;
+};
+constexpr int64_t kMaxAdamwElems = int64_t(1) << 40;  // of one tensor
+constexpr uint32_t kMaxAdamwGroups = 1u << 30;        // workgroups of a launch
+// t, on the host, is read before the call returns.
+hipError_t launch_adamw(const AdamwTensor *t, int count, bool p_f32, bool g_f32, bool bits8, bool master,
+                        const AdamwHyper &h, hipStream_t s);
+// The fp32 values of 8-bit states, written to param (m) and grad (v).
+hipError_t launch_adamw_moments(const AdamwTensor *t, int count, hipStream_t s);
+
 }  // namespace qnf4

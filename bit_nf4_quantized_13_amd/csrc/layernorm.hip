@@ -1,0 +1,405 @@
+// Layer norm over the rows of x [M x n], and its backward:
+//   mu = sum(x) / n      rstd = (sum((x - mu)^2) / n + eps)^-1/2
+//   y  = (x - mu) rstd w + b
+//   xh = (x - mu) rstd   g = dy w
+//   dx = rstd (g - mean(g) - xh mean(g xh))
+//   dw = sum over rows of dy xh      db = sum over rows of dy
+//
+// Statistics and sums in fp32 whatever x's type: mu first, then the squares of
+// the deviations from it (both from registers), so a row whose mean is far
+// larger than its spread keeps its variance; one rounding at the store.
+//
+// Bound: HBM (8 to 14 flops an element).  x (and dy) are read once and held in
+// registers over the reductions: a row is spread over TPR threads of 8 NV
+// elements each, TPR and NV the smallest that hold n; 256 threads take
+// 256 / TPR rows at a time.  Rows wider than kMaxHeld go through a kernel that
+// reads them again for each reduction (from L2).
+//
+// dw and db add over all rows: a workgroup of 1024 threads walks the rows with
+// its columns' sums in registers, adds its row groups' sums in LDS and writes
+// one partial row, and a second kernel adds the partial rows: fixed orders, so
+// the same bits on every run.
+#include "elem8.hpp"
+#include "launch.hpp"
+
+namespace qnf4 {
+namespace {
+
+constexpr int64_t kMaxHeld = 16384;    // widest row held in registers
+constexpr int kGradThreads = 1024;     // workgroup of the backward with parameter gradients
+constexpr int kMaxPartials = 256;      // its partial rows: one workgroup a CU
+constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
+
+// Sum of v over the TPR threads of a row group (TPR a multiple of 64); every
+// thread of the workgroup calls it.  red: one float for each wave.
+template <int TPR>
+__device__ __forceinline__ float group_sum(float v, float *red) {
+    v = wave_sum(v);
+    if (TPR == 64) return v;
+    const int wave = threadIdx.x >> 6, w0 = threadIdx.x / TPR * (TPR / 64);
+    __syncthreads();  // the last reading of red is done
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) s += red[w0 + i];
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ F8 param8(const T *p, int64_t c, int64_t n, float fill) {
+    F8 r;
+    if (p) return load8(p + c, n - c, fill);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = fill;
+    return r;
+}
+
+template <typename T, typename W, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(
+    const T *__restrict__ x, int64_t M, int64_t n, int64_t ldx, const W *__restrict__ w, const W *__restrict__ b,
+    float eps, T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
+    constexpr int kThreads = TPR > 256 ? TPR : 256;
+    __shared__ float red[kThreads / 64];
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    const bool live = row < M;
+    const float inv_n = 1.0f / (float)n;
+    F8 v[NV];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * TPR + t) * 8;
+        v[i] = load8(x + row * ldx + c, live ? n - c : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[i].v[e];
+    }
+    const float mu = group_sum<TPR>(s, red) * inv_n;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * TPR + t) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[i].v[e] -= mu;
+            if (c + e < n) q += v[i].v[e] * v[i].v[e];
+        }
+    }
+    const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red) * inv_n + eps);
+    if (!live) return;
+    if (t == 0 && mean) mean[row] = mu;
+    if (t == 0 && rstd) rstd[row] = rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * TPR + t) * 8;
+        if (c >= n) break;
+        const F8 wv = param8(w, c, n, 1.0f), bv = param8(b, c, n, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i].v[e] = v[i].v[e] * rs * wv.v[e] + bv.v[e];
+        store8(y + row * n + c, n - c, v[i]);
+    }
+}
+
+// Rows wider than the registers hold: one workgroup a row, read three times.
+template <typename T, typename W>
+__global__ __launch_bounds__(kStreamThreads) void norm_fwd_stream_kernel(
+    const T *__restrict__ x, int64_t n, int64_t ldx, const W *__restrict__ w, const W *__restrict__ b, float eps,
+    T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
+    __shared__ float red[kStreamThreads / 64];
+    const int64_t row = blockIdx.x;
+    const T *xr = x + row * ldx;
+    const float inv_n = 1.0f / (float)n;
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
+        const F8 v = load8(xr + c, n - c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v.v[e];
+    }
+    const float mu = group_sum<kStreamThreads>(s, red) * inv_n;
+    float q = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
+        const F8 v = load8(xr + c, n - c, mu);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q += (v.v[e] - mu) * (v.v[e] - mu);
+    }
+    const float rs = 1.0f / sqrtf(group_sum<kStreamThreads>(q, red) * inv_n + eps);
+    if (threadIdx.x == 0 && mean) mean[row] = mu;
+    if (threadIdx.x == 0 && rstd) rstd[row] = rs;
+    for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
+        F8 v = load8(xr + c, n - c);
+        const F8 wv = param8(w, c, n, 1.0f), bv = param8(b, c, n, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = (v.v[e] - mu) * rs * wv.v[e] + bv.v[e];
+        store8(y + row * n + c, n - c, v);
+    }
+}
+
+// dX, and with GRAD the workgroup's partial row of dw and db ([2][n] at
+// part + blockIdx.x 2 n).  Row group g of the workgroup takes the rows
+// blockIdx.x GROUPS + g, then every gridDim.x GROUPS-th.
+template <typename T, typename W, int THREADS, int TPR, int NV, bool GRAD>
+__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
+    const T *__restrict__ x, const T *__restrict__ dy, int64_t M, int64_t n, int64_t ldx,
+    const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx,
+    float *__restrict__ part) {
+    constexpr int kGroups = THREADS / TPR;
+    __shared__ float red1[THREADS / 64], red2[THREADS / 64];
+    const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
+    const float inv_n = 1.0f / (float)n;
+    F8 dw[GRAD ? NV : 1], db[GRAD ? NV : 1];
+    if (GRAD) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dw[i].v[e] = db[i].v[e] = 0.0f;
+    }
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < M; r0 += step) {
+        const int64_t row = r0 + g;
+        const bool live = row < M;
+        const float mu = live ? mean[row] : 0.0f, rs = live ? rstd[row] : 0.0f;
+        F8 xh[NV], gr[NV];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = ((int64_t)i * TPR + t) * 8;
+            xh[i] = load8(x + row * ldx + c, live ? n - c : 0, mu);
+            gr[i] = load8(dy + row * n + c, live ? n - c : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = ((int64_t)i * TPR + t) * 8;
+            const F8 wv = param8(w, c, n, 1.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = (xh[i].v[e] - mu) * rs, d = gr[i].v[e];
+                if (GRAD) {
+                    dw[i].v[e] += d * h;
+                    db[i].v[e] += d;
+                }
+                xh[i].v[e] = h;
+                gr[i].v[e] = d * wv.v[e];
+                s1 += gr[i].v[e];
+                s2 += gr[i].v[e] * h;
+            }
+        }
+        const float c1 = group_sum<TPR>(s1, red1) * inv_n, c2 = group_sum<TPR>(s2, red2) * inv_n;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = ((int64_t)i * TPR + t) * 8;
+                F8 o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.v[e] = rs * (gr[i].v[e] - c1 - xh[i].v[e] * c2);
+                if (c < n) store8(dx + row * n + c, n - c, o);
+            }
+        }
+    }
+    if (!GRAD) return;
+    // the row groups' sums, added in group order
+    extern __shared__ float sums[];  // [2][n], where there is more than one group
+    float *out = part + (int64_t)blockIdx.x * 2 * n;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        if (g == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = ((int64_t)i * TPR + t) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (c + e >= n) continue;
+                    float a = dw[GRAD ? i : 0].v[e], d = db[GRAD ? i : 0].v[e];
+                    if (k > 0) {
+                        a += sums[c + e];
+                        d += sums[n + c + e];
+                    }
+                    if (k + 1 < kGroups) {
+                        sums[c + e] = a;
+                        sums[n + c + e] = d;
+                    } else {
+                        out[c + e] = a;
+                        out[n + c + e] = d;
+                    }
+                }
+            }
+        }
+        if (k + 1 < kGroups) __syncthreads();
+    }
+}
+
+// Wide rows' dX: one workgroup a row, read twice.
+template <typename T, typename W>
+__global__ __launch_bounds__(kStreamThreads) void norm_bwd_stream_kernel(
+    const T *__restrict__ x, const T *__restrict__ dy, int64_t n, int64_t ldx, const float *__restrict__ mean,
+    const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx) {
+    __shared__ float red1[kStreamThreads / 64], red2[kStreamThreads / 64];
+    const int64_t row = blockIdx.x;
+    const T *xr = x + row * ldx, *dr = dy + row * n;
+    const float mu = mean[row], rs = rstd[row], inv_n = 1.0f / (float)n;
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
+        const F8 xv = load8(xr + c, n - c, mu), dv = load8(dr + c, n - c), wv = param8(w, c, n, 1.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float gv = dv.v[e] * wv.v[e];
+            s1 += gv;
+            s2 += gv * ((xv.v[e] - mu) * rs);
+        }
+    }
+    const float c1 = group_sum<kStreamThreads>(s1, red1) * inv_n, c2 = group_sum<kStreamThreads>(s2, red2) * inv_n;
+    for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
+        const F8 xv = load8(xr + c, n - c, mu), dv = load8(dr + c, n - c), wv = param8(w, c, n, 1.0f);
+        F8 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.v[e] = rs * (dv.v[e] * wv.v[e] - c1 - (xv.v[e] - mu) * rs * c2);
+        store8(dx + row * n + c, n - c, o);
+    }
+}
+
+// Wide rows' dw and db: a workgroup takes 8 columns a thread and every
+// gridDim.y-th row, into partial row blockIdx.y.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_cols_kernel(const T *__restrict__ x, const T *__restrict__ dy, int64_t M,
+                                                        int64_t n, int64_t ldx, const float *__restrict__ mean,
+                                                        const float *__restrict__ rstd, float *__restrict__ part) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c >= n) return;
+    F8 dw, db;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw.v[e] = db.v[e] = 0.0f;
+    for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
+        const float mu = mean[row], rs = rstd[row];
+        const F8 xv = load8(x + row * ldx + c, n - c), dv = load8(dy + row * n + c, n - c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dw.v[e] += dv.v[e] * ((xv.v[e] - mu) * rs);
+            db.v[e] += dv.v[e];
+        }
+    }
+    float *out = part + (int64_t)blockIdx.y * 2 * n;
+    store8(out + c, n - c, dw);
+    store8(out + n + c, n - c, db);
+}
+
+// dw and db from the partial rows: 64 columns of [dw | db] a workgroup, its 16
+// waves a sixteenth of the rows each, added in wave order.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restrict__ part, int parts, int64_t n,
+                                                           float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float sums[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (c < 2 * n)
+        for (int p = wave; p < parts; p += 16) s += part[(int64_t)p * 2 * n + c];
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= 2 * n) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += sums[i][lane];
+    if (c < n) {
+        if (dw) dw[c] = s;
+    } else if (db) {
+        db[c - n] = s;
+    }
+}
+
+// The threads and groups of 8 a row of n takes, passed on as template values.
+template <typename F>
+hipError_t held_shape(int64_t n, F f) {
+    if (n <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+    if (n <= 1024) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    if (n <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
+    if (n <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+    if (n <= 8192) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+}
+
+template <typename T, typename W>
+hipError_t norm_fwd(const T *x, int64_t M, int64_t n, int64_t ldx, const W *w, const W *b, float eps, T *y,
+                    float *mean, float *rstd, hipStream_t s) {
+    if (n > kMaxHeld) {
+        norm_fwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, n, ldx, w, b, eps, y, mean, rstd);
+        return hipGetLastError();
+    }
+    return held_shape(n, [&](auto tpr, auto nv) {
+        constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
+        norm_fwd_kernel<T, W, kTpr, decltype(nv)::value>
+            <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, M, n, ldx, w, b, eps, y, mean, rstd);
+        return hipGetLastError();
+    });
+}
+
+template <typename T, typename W>
+hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, const float *mean, const float *rstd,
+                    const W *w, T *dx, float *dw, float *db, float *part, hipStream_t s) {
+    const bool grad = dw || db;
+    int parts = 0;
+    hipError_t e;
+    if (n > kMaxHeld) {
+        norm_bwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, dy, n, ldx, mean, rstd, w, dx);
+        e = hipGetLastError();
+        if (!grad || e != hipSuccess) return e;
+        parts = M < kMaxPartials ? (int)M : kMaxPartials;
+        norm_cols_kernel<T><<<dim3((unsigned)((n + 2047) / 2048), parts), 256, 0, s>>>(x, dy, M, n, ldx, mean, rstd, part);
+        e = hipGetLastError();
+    } else {
+        e = held_shape(n, [&](auto tpr, auto nv) {
+            constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
+            if (!grad) {
+                constexpr int kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
+                norm_bwd_kernel<T, W, kThreads, kTpr, kNv, false>
+                    <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr);
+                return hipGetLastError();
+            }
+            constexpr int kRows = kGradThreads / kTpr;
+            const int64_t groups = (M + kRows - 1) / kRows;
+            parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
+            const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 64 KiB
+            auto *kernel = norm_bwd_kernel<T, W, kGradThreads, kTpr, kNv, true>;
+            const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+            if (err != hipSuccess) return err;
+            kernel<<<parts, kGradThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part);
+            return hipGetLastError();
+        });
+    }
+    if (!grad || e != hipSuccess) return e;
+    norm_reduce_kernel<<<(unsigned)((2 * n + 63) / 64), 1024, 0, s>>>(part, parts, n, dw, db);
+    return hipGetLastError();
+}
+
+// f with x's and the weight's element types.
+template <typename F>
+hipError_t typed(bool x_f32, bool w_f32, F f) {
+    if (x_f32) return w_f32 ? f((float *)nullptr, (float *)nullptr) : f((float *)nullptr, (uint16_t *)nullptr);
+    return w_f32 ? f((uint16_t *)nullptr, (float *)nullptr) : f((uint16_t *)nullptr, (uint16_t *)nullptr);
+}
+
+}  // namespace
+
+size_t layernorm_part_bytes(int64_t M, int64_t n) {
+    return sizeof(float) * 2 * (size_t)n * (size_t)(M < kMaxPartials ? M : kMaxPartials);
+}
+
+hipError_t launch_layernorm_fwd(const void *x, bool x_f32, int64_t M, int64_t n, int64_t ldx, const void *w,
+                                const void *b, bool w_f32, float eps, void *y, float *mean, float *rstd,
+                                hipStream_t s) {
+    return typed(x_f32, w_f32, [&](auto *tx, auto *tw) {
+        using T = std::remove_pointer_t<decltype(tx)>;
+        using W = std::remove_pointer_t<decltype(tw)>;
+        return norm_fwd<T, W>((const T *)x, M, n, ldx, (const W *)w, (const W *)b, eps, (T *)y, mean, rstd, s);
+    });
+}
+
+hipError_t launch_layernorm_bwd(const void *x, const void *dy, bool x_f32, int64_t M, int64_t n, int64_t ldx,
+                                const float *mean, const float *rstd, const void *w, bool w_f32, void *dx, float *dw,
+                                float *db, float *part, hipStream_t s) {
+    return typed(x_f32, w_f32, [&](auto *tx, auto *tw) {
+        using T = std::remove_pointer_t<decltype(tx)>;
+        using W = std::remove_pointer_t<decltype(tw)>;
+        return norm_bwd<T, W>((const T *)x, (const T *)dy, M, n, ldx, mean, rstd, (const W *)w, (T *)dx, dw, db, part, s);
+    });
+}
+
+}  // namespace qnf4

@@ -376,6 +376,142 @@ int qlora_adapter_merge(const qlora_nf4_weight *w, const qlora_bf16 *A, const ql
 int qlora_adapter_unmerge(const qlora_bf16 *W_in, int64_t d, int64_t k, const qlora_bf16 *A, const qlora_bf16 *B,
                           int32_t r, float alpha, qlora_bf16 *W_out, void *stream);
 
+/* ---- the operators around the linear layer in a fine-tuning step ------------
+ *
+ * Element types of their arrays; every pointer is aligned to its element, rows
+ * and views may start anywhere beyond that.
+ */
+#define QLORA_BF16 0
+#define QLORA_F32  1
+
+/*
+ * qlora_layernorm_fwd -- y = (x - mu) rstd w + b over rows of n elements, with
+ * mu the row's mean and rstd = (mean((x - mu)^2) + eps)^-1/2, both in fp32.
+ *   x       device [M x n] of x_type, rows ldx >= n elements apart
+ *   weight, bias  device [n] of w_type, or NULL (1 and 0)
+ *   eps     >= 0
+ *   y       device [M x n] of x_type, dense, written
+ *   mean, rstd  device fp32 [M], written, or NULL
+ * Errors: QLORA_EINVAL (null pointer, size <= 0, ldx < n, eps), QLORA_ENOTSUP
+ * (unknown type, M >= 2^31, n > 2^30), QLORA_EALIGN (a pointer not aligned to
+ * its element).
+ */
+int qlora_layernorm_fwd(const void *x, int32_t x_type, int64_t M, int64_t n, int64_t ldx, const void *weight,
+                        const void *bias, int32_t w_type, float eps, void *y, float *mean, float *rstd,
+                        void *stream);
+
+/* Bytes of device workspace qlora_layernorm_bwd needs when it is given dweight
+ * or dbias (0 for invalid arguments). */
+size_t qlora_layernorm_workspace(int64_t M, int64_t n);
+
+/*
+ * qlora_layernorm_bwd -- the gradients of qlora_layernorm_fwd.  With
+ * xh = (x - mu) rstd and g = dy w:
+ *   dx = rstd (g - mean(g) - xh mean(g xh))    dweight = sum over rows of dy xh
+ *   dbias = sum over rows of dy
+ *   x, weight as in the forward; mean, rstd its outputs
+ *   dy      device [M x n] of x_type, dense;  dx likewise, written
+ *   dweight, dbias  device fp32 [n], written, or NULL to skip them (a frozen norm)
+ *   ws      >= qlora_layernorm_workspace(M, n) bytes with dweight or dbias, else unused.
+ * Rows are added in a fixed order: the same bits on every run.
+ */
+int qlora_layernorm_bwd(const void *x, const void *dy, int32_t x_type, int64_t M, int64_t n, int64_t ldx,
+                        const float *mean, const float *rstd, const void *weight, int32_t w_type, void *dx,
+                        float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace qlora_logprob_fwd needs (0 for invalid arguments). */
+size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top);
+
+/*
+ * qlora_logprob_fwd -- log-probabilities of given tokens under rows of logits,
+ * the rows' entropies and their best alternatives:
+ *   lse[m]     = log sum_v e^x[m][v]
+ *   logp[m]    = x[m][targets[m]] - lse[m]
+ *   entropy[m] = -sum_v p[m][v] log p[m][v],  p = e^(x - lse)
+ *   top_ids[m][i], top_logp[m][i]: the i-th largest logit's index and x - lse,
+ *                equal logits in ascending order of index
+ *   logits  device [M x V] of `type`, rows ld >= V elements apart; V <= 2^19
+ *   targets device int64 [M]; a target outside [0, V) marks a row without one: logp = 0
+ *   top     0..16 alternatives, at most V
+ *   logp (with targets, else both NULL), entropy, lse  device fp32 [M] or NULL
+ *   top_logp fp32, top_ids int32 device [M x top] (top > 0)
+ *   ws      >= qlora_logprob_workspace(M, V, top) bytes.
+ * A logit of -inf is a token that is ruled out: p = 0.  A row of -inf alone has
+ * lse = -inf, logp = -inf, entropy 0 and alternatives of -inf at the lowest
+ * indices.  Logits are otherwise finite.
+ * Errors: QLORA_EINVAL (null pointer, size <= 0, ld < V, top > V), QLORA_ENOTSUP
+ * (unknown type, V > 2^19, top > 16, too many rows for one launch), QLORA_EALIGN,
+ * QLORA_EWORKSPACE.
+ */
+int qlora_logprob_fwd(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                      int32_t top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
+                      void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * qlora_logprob_bwd -- the gradient of qlora_logprob_fwd's logp and entropy:
+ *   dlogits[m][v] = dlogp[m] ((v == targets[m]) - p) - dentropy[m] p (log p + entropy[m])
+ * rounded once to `type`.  Ruled-out tokens and rows get 0.
+ *   lse, entropy  the forward's outputs (entropy only with dentropy)
+ *   dlogp (with targets), dentropy  device fp32 [M]; either may be NULL, not both
+ *   dlogits device [M x V] of `type`, rows ldd >= V elements apart, written; may be
+ *           the logits themselves (then ldd == ld).
+ * Rows whose |lse| exceeds 4096, too large to hold log p's digits, are summed
+ * again inside the call and p normalised by that.
+ */
+int qlora_logprob_bwd(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                      const float *lse, const float *entropy, const float *dlogp, const float *dentropy,
+                      void *dlogits, int64_t ldd, void *stream);
+
+#define QLORA_STATE_F32  0
+#define QLORA_STATE_8BIT 1
+#define QLORA_STATE_BLOCK 256  /* elements that share the scales of 8-bit states */
+
+/* One tensor of an AdamW step: dense device arrays of n elements. */
+typedef struct {
+    void *param;        /* of param_type, updated (bf16 with a master: written only) */
+    const void *grad;   /* of grad_type */
+    void *m, *v;        /* fp32, or int8 (m) and uint8 (v) codes; updated */
+    float *m_scale;     /* 8-bit states: fp32 [ceil(n / 256)] each, updated; else NULL */
+    float *v_scale;
+    float *master;      /* with use_master: the fp32 weights, updated; else NULL */
+    int64_t n;          /* 0: left out */
+} qlora_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    double grad_scale;  /* the stored gradients are multiplied by it (1: as they are) */
+    int64_t step;       /* this step's number, from 1 */
+    int32_t param_type, grad_type;  /* QLORA_BF16 or QLORA_F32 */
+    int32_t state_type;             /* QLORA_STATE_F32 or QLORA_STATE_8BIT */
+    int32_t use_master;             /* bf16 param with fp32 master weights */
+} qlora_adamw_config;
+
+/*
+ * qlora_adamw_step -- one AdamW step (decoupled weight decay) over `count` tensors:
+ *   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, each state and weight rounded once where it is stored.  The two
+ * structs are HOST memory, read before the call returns; a captured graph
+ * replays this step's number and rates.
+ * 8-bit states, in blocks of 256 elements (the last may be shorter) with fp32 scales s:
+ *   m = sign(c) c^2 s, c in [-127, 127], s = fp32(max|m| fp32(127^-2)), c = rint(sqrt(fp32(|m| fp32(1/s))))
+ *   v = c^4 s,         c in [0, 255],    s = fp32(max v fp32(255^-4)),  c = rint(sqrt(sqrt(fp32(v fp32(1/s)))))
+ *                                        and c >= 1 where v > 0
+ * (IEEE fp32 operations; a scale below the smallest normal number becomes 0
+ * and its block zeros).  Zeroed codes and scales are the states at the start.
+ * Errors: QLORA_EINVAL (null pointer, n < 0, step < 1, a rate out of range,
+ * master without use_master or the reverse, use_master with fp32 param),
+ * QLORA_ENOTSUP (unknown type, n > 2^40), QLORA_EALIGN.
+ */
+int qlora_adamw_step(const qlora_adamw_tensor *tensors, int32_t count, const qlora_adamw_config *config,
+                     void *stream);
+
+/* qlora_adamw_moments -- the fp32 values that 8-bit states stand for: tensor i's
+ * to m_out[i] and v_out[i] (HOST arrays of device fp32 [n] pointers).  Only m,
+ * v, their scales and n of the tensors are used. */
+int qlora_adamw_moments(const qlora_adamw_tensor *tensors, int32_t count, float *const *m_out, float *const *v_out,
+                        void *stream);
+
 /*
  * qlora_nf4_codebook -- host-only: copies the library's 16 fp32 NF4 levels
  * (chkda, "NF4: Choose the codebook to fit the distribution"; built as in
@@ -397,7 +533,7 @@ const char *qlora_status_str(int status);
 
 /* ABI version of this header/library pair. */
 int qlora_abi_version(void);
-#define QLORA_ABI_VERSION 6
+#define QLORA_ABI_VERSION 7
 
 #ifdef __cplusplus
 }

@@ -20,5 +20,6 @@ Modules:
   nf4    -- codebook, blockwise NF4 quantize/dequantize, Int8 absmax,
             double quantization and doubleDequant (bit-exact contracts).
   qlora  -- the linear layer forward and backward in float64.
+  step   -- the operators around it in a fine-tuning step, in float64.
 """
-from . import nf4, qlora  # noqa: F401
+from . import nf4, qlora, step  # noqa: F401

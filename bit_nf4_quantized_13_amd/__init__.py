@@ -17,6 +17,8 @@ and, around the linear layer in a fine-tuning step:
 
     qlora_layernorm_fwd(x, weight, bias)      -> (y, mean, rstd)
     qlora_layernorm_bwd(x, dy, mean, rstd, weight) -> (dx, dweight, dbias)
+    qlora_attention_fwd(q, k, v, cu_seqlens)  -> (o, lse, residual)
+    qlora_attention_bwd(q, k, v, o, lse, dout, cu_seqlens) -> (dq, dk, dv)
     qlora_logprob_fwd(logits, targets, top)   -> (logp, entropy, lse, top_logp, top_ids)
     qlora_logprob_bwd(logits, targets, lse, entropy, dlogp, dentropy) -> dlogits
     qlora_adamw_step(AdamWPlan(params, grads, m, v, ...), lr=..., step=...)
@@ -68,6 +70,12 @@ class _CAdamWConfig(ctypes.Structure):
                 ("state_type", ctypes.c_int32), ("use_master", ctypes.c_int32)]
 
 
+class _CAttentionShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("sequences", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("ldq", ctypes.c_int64),
+                ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -103,6 +111,10 @@ _SIGS = {
     "qlora_layernorm_workspace": (_SZ, [_I64, _I64]),
     "qlora_layernorm_bwd": (ctypes.c_int, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _P, _SZ,
                                            _P]),
+    "qlora_attention_fwd": (ctypes.c_int, [ctypes.POINTER(_CAttentionShape), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "qlora_attention_workspace": (_SZ, [ctypes.POINTER(_CAttentionShape)]),
+    "qlora_attention_bwd": (ctypes.c_int, [ctypes.POINTER(_CAttentionShape), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
+                                           _P, _I64, _P, _I64, _P, _SZ, _P]),
     "qlora_logprob_workspace": (_SZ, [_I64, _I64, _I32]),
     "qlora_logprob_fwd": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "qlora_logprob_bwd": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _P]),
@@ -509,6 +521,80 @@ def layernorm_workspace_bytes(m: int, n: int) -> int:
     return int(_lib.qlora_layernorm_workspace(m, n))
 
 
+def _heads(t: torch.Tensor, rows: int, dim: int, name: str) -> int:
+    """The row pitch, in elements, of a device bf16 [rows, heads, dim] whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [{rows}, heads, {dim}], got {list(t.shape)}")
+    width = t.shape[1] * dim
+    if (dim > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have its heads side by side in dense rows")
+    if rows > 1 and t.stride(0) < width:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0) if rows > 1 else width
+
+
+def _attention_shape(q, k, v, cu_seqlens, scale) -> _CAttentionShape:
+    if q.dim() != 3:
+        raise ValueError("q must have shape [rows, heads, dim]")
+    rows, heads, dim = q.shape
+    ldq, ldk, ldv = (_heads(t, rows, dim, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    if k.shape[1] != v.shape[1]:
+        raise ValueError("k and v must have the same heads")
+    _dev_tensor(cu_seqlens, torch.int32, "cu_seqlens")
+    return _CAttentionShape(rows, cu_seqlens.numel() - 1, heads, k.shape[1], dim, ldq, ldk, ldv,
+                            dim ** -0.5 if scale is None else scale)
+
+
+def qlora_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                        scale: float | None = None, save_residual: bool = False, out: torch.Tensor | None = None):
+    """Causal attention over packed sequences: q bf16 [T, heads, dim], k and v [T, kv_heads, dim] (rows at
+    any pitch of a multiple of 8), sequence s in the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32).
+    Returns (o like q, lse fp32 [heads, T], residual like o or None); the residual is what the backward
+    takes to be exact in o.  scale: dim ** -0.5 if not given."""
+    shape = _attention_shape(q, k, v, cu_seqlens, scale)
+    o = _shaped(out, torch.bfloat16, q.shape, "out") if out is not None else torch.empty(
+        q.shape, dtype=torch.bfloat16, device=q.device)
+    res = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if save_residual else None
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    _check(_lib.qlora_attention_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                    cu_seqlens.data_ptr(), o.data_ptr(), _ptr(res), lse.data_ptr(), _stream()),
+           "qlora_attention_fwd")
+    return o, lse, res
+
+
+def qlora_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                        dout: torch.Tensor, cu_seqlens: torch.Tensor, scale: float | None = None,
+                        residual: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        outs: tuple | None = None):
+    """(dq, dk, dv) like q, k, v from the forward's o, lse (and residual) and dout; outs may be slices
+    of one matrix."""
+    shape = _attention_shape(q, k, v, cu_seqlens, scale)
+    _shaped(o, torch.bfloat16, q.shape, "o")
+    _shaped(dout, torch.bfloat16, q.shape, "dout")
+    _shaped(lse, torch.float32, (q.shape[1], q.shape[0]), "lse")
+    if residual is not None:
+        _shaped(residual, torch.bfloat16, q.shape, "residual")
+    dq, dk, dv = outs if outs is not None else (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
+                                                for t in (q, k, v))
+    rows, _, dim = q.shape
+    pitches = []
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {list(like.shape)}")
+        pitches.append(_heads(t, rows, dim, name))
+    ws = workspace if workspace is not None else _workspace(
+        int(_lib.qlora_attention_workspace(ctypes.byref(shape))), q.device)
+    _check(_lib.qlora_attention_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                    _ptr(residual), lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(),
+                                    dq.data_ptr(), pitches[0], dk.data_ptr(), pitches[1], dv.data_ptr(), pitches[2],
+                                    ws.data_ptr(), ws.numel(), _stream()), "qlora_attention_bwd")
+    return dq, dk, dv
+
+
 def logprob_workspace_bytes(m: int, v: int, top: int = 0) -> int:
     return int(_lib.qlora_logprob_workspace(m, v, top))
 
@@ -635,6 +721,7 @@ def qlora_adamw_moments(plan: AdamWPlan, m_out=None, v_out=None):
 
 __all__ = [
     "qlora_layernorm_fwd", "qlora_layernorm_bwd", "layernorm_workspace_bytes",
+    "qlora_attention_fwd", "qlora_attention_bwd",
     "qlora_logprob_fwd", "qlora_logprob_bwd", "logprob_workspace_bytes",
     "AdamWPlan", "qlora_adamw_step", "qlora_adamw_moments", "STATE_BLOCK",
     "NF4Weight", "QloraError", "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",

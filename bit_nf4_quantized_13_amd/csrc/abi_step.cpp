@@ -1,5 +1,5 @@
 // The C ABI of the operators around the linear layer in a fine-tuning step
-// (include/qlora_nf4.h): layer norm, token log-probabilities, AdamW.  As in
+// (include/qlora_nf4.h): layer norm, attention, token log-probabilities, AdamW.  As in
 // abi.cpp every check runs before the first launch; no allocation, no
 // synchronisation, no state.
 #include "qlora_nf4.h"
@@ -27,6 +27,30 @@ int check_norm(const void *x, int32_t x_type, int64_t M, int64_t n, int64_t ldx,
     if (M > kMaxRows || n > kMaxNormWidth) return QLORA_ENOTSUP;
     if (!aligned(x, type_bytes(x_type)) || !aligned_or_null(weight, type_bytes(w_type))) return QLORA_EALIGN;
     return QLORA_OK;
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // row numbers and tile ends stay below 2^31
+constexpr int64_t kMaxPitch = int64_t(1) << 23;   // 64 rows of a tile lie within 2^30 bytes
+
+// A matrix of `width` values a row: pitch and alignment of 16-byte accesses.
+int check_pitch(int64_t ld, int64_t width) {
+    if (ld < width) return QLORA_EINVAL;
+    return ld % 8 == 0 && ld <= kMaxPitch ? QLORA_OK : QLORA_ENOTSUP;
+}
+
+int check_attention(const qlora_attention_shape *s, AttentionShape *a) {
+    if (!s) return QLORA_EINVAL;
+    if (s->T <= 0 || s->sequences <= 0 || s->heads <= 0 || s->kv_heads <= 0 || s->dim <= 0) return QLORA_EINVAL;
+    if (s->heads % s->kv_heads != 0 || !(s->scale > 0.0f) || std::isinf(s->scale)) return QLORA_EINVAL;
+    if (s->dim % 8 != 0 || s->dim > 128 || s->T > kMaxTokens || s->sequences > kMaxTokens) return QLORA_ENOTSUP;
+    const int64_t wide = (int64_t)s->heads * s->dim, narrow = (int64_t)s->kv_heads * s->dim;
+    if (wide > kMaxPitch) return QLORA_ENOTSUP;  // the dense rows of o
+    int st = check_pitch(s->ldq, wide);
+    if (st == QLORA_OK) st = check_pitch(s->ldk, narrow);
+    if (st == QLORA_OK) st = check_pitch(s->ldv, narrow);
+    if (st != QLORA_OK) return st;
+    *a = AttentionShape{(int)s->T, s->sequences, s->heads, s->kv_heads, s->dim, s->ldq, s->ldk, s->ldv, s->scale};
+    return attention_groups(*a) <= kMaxRows ? QLORA_OK : QLORA_ENOTSUP;
 }
 
 int check_logits(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld) {
@@ -98,6 +122,51 @@ int qlora_layernorm_bwd(const void *x, const void *dy, int32_t x_type, int64_t M
     return hip_status(launch_layernorm_bwd(x, dy, x_type == QLORA_F32, M, n, ldx, mean, rstd, weight,
                                            w_type == QLORA_F32, dx, dweight, dbias, static_cast<float *>(ws),
                                            static_cast<hipStream_t>(stream)));
+}
+
+int qlora_attention_fwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
+                        const qlora_bf16 *v, const int32_t *cu_seqlens, qlora_bf16 *o, qlora_bf16 *residual,
+                        float *lse, void *stream) {
+    AttentionShape a;
+    const int st = check_attention(shape, &a);
+    if (st != QLORA_OK) return st;
+    if (!q || !k || !v || !cu_seqlens || !o || !lse) return QLORA_EINVAL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned_or_null(residual, 16) ||
+        !aligned(cu_seqlens, 4) || !aligned(lse, 4))
+        return QLORA_EALIGN;
+    (void)hipGetLastError();
+    return hip_status(launch_attention_fwd(a, q, k, v, cu_seqlens, o, residual, lse, static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_attention_workspace(const qlora_attention_shape *shape) {
+    AttentionShape a;
+    if (check_attention(shape, &a) != QLORA_OK) return 0;
+    return round_up(sizeof(float) * (size_t)a.T * a.H, 256);  // delta
+}
+
+int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
+                        const qlora_bf16 *v, const qlora_bf16 *o, const qlora_bf16 *residual, const float *lse,
+                        const qlora_bf16 *dout, const int32_t *cu_seqlens, qlora_bf16 *dq, int64_t lddq,
+                        qlora_bf16 *dk, int64_t lddk, qlora_bf16 *dv, int64_t lddv, void *ws, size_t ws_bytes,
+                        void *stream) {
+    AttentionShape a;
+    int st = check_attention(shape, &a);
+    if (st != QLORA_OK) return st;
+    if (!q || !k || !v || !o || !lse || !dout || !cu_seqlens || !dq || !dk || !dv) return QLORA_EINVAL;
+    const int64_t wide = (int64_t)a.H * a.D, narrow = (int64_t)a.Hk * a.D;
+    st = check_pitch(lddq, wide);
+    if (st == QLORA_OK) st = check_pitch(lddk, narrow);
+    if (st == QLORA_OK) st = check_pitch(lddv, narrow);
+    if (st != QLORA_OK) return st;
+    for (const void *p : {(const void *)q, (const void *)k, (const void *)v, (const void *)o, (const void *)residual,
+                          (const void *)dout, (const void *)dq, (const void *)dk, (const void *)dv})
+        if (!aligned_or_null(p, 16)) return QLORA_EALIGN;
+    if (!aligned(cu_seqlens, 4) || !aligned(lse, 4)) return QLORA_EALIGN;
+    if (!ws || ws_bytes < qlora_attention_workspace(shape)) return QLORA_EWORKSPACE;
+    if (!aligned(ws, 16)) return QLORA_EALIGN;
+    (void)hipGetLastError();
+    return hip_status(launch_attention_bwd(a, q, k, v, o, residual, lse, dout, cu_seqlens, dq, lddq, dk, lddk, dv, lddv,
+                                           static_cast<float *>(ws), static_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top) {

@@ -222,4 +222,20 @@ hipError_t launch_adamw(const AdamwTensor *t, int count, bool p_f32, bool g_f32,
 // The fp32 values of 8-bit states, written to param (m) and grad (v).
 hipError_t launch_adamw_moments(const AdamwTensor *t, int count, hipStream_t s);
 
+// ---- causal attention over packed sequences (attention.hip) ------------------------
+struct AttentionShape {
+    int T, S;                   // rows, sequences
+    int H, Hk, D;               // heads, key-value heads, head dimension (a multiple of 8, at most 128)
+    int64_t ldq, ldk, ldv;      // row pitches, in elements
+    float scale;
+};
+int64_t attention_groups(const AttentionShape &a);  // workgroups of the largest launch
+// cu: S + 1 starts on the device; o, res, dout dense [T x H x D] (res may be null); lse, delta [H x T].
+hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s);
+hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout,
+                                const int32_t *cu, uint16_t *dq, int64_t lddq, uint16_t *dk, int64_t lddk,
+                                uint16_t *dv, int64_t lddv, float *delta, hipStream_t s);
+
 }  // namespace qnf4

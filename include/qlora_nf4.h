@@ -419,6 +419,60 @@ int qlora_layernorm_bwd(const void *x, const void *dy, int32_t x_type, int64_t M
                         const float *mean, const float *rstd, const void *weight, int32_t w_type, void *dx,
                         float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
+/* Causal attention over packed sequences: sizes and row pitches. */
+typedef struct {
+    int64_t T;               /* rows of q, k, v */
+    int32_t sequences;       /* cu_seqlens holds sequences + 1 entries */
+    int32_t heads, kv_heads; /* heads a multiple of kv_heads */
+    int32_t dim;             /* of a head: a multiple of 8, at most 128 */
+    int64_t ldq, ldk, ldv;   /* elements between rows, multiples of 8 */
+    float scale;             /* of the scores, > 0 (usually dim^-1/2) */
+} qlora_attention_shape;
+
+/*
+ * qlora_attention_fwd -- softmax attention of every row over the rows of its own
+ * sequence up to itself.  Sequence s holds the rows cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1 (ascending; any length, 0 included); head h reads the
+ * key-value head h / (heads / kv_heads).  With j over those rows:
+ *   lse[h][i] = log sum_j e^(scale q_i k_j)      o_i = sum_j e^(scale q_i k_j - lse) v_j
+ * Rows that belong to no sequence get o = 0 and lse = -inf.
+ *   q      device bf16, row i at q + i ldq, its heads' dim values side by side;
+ *          k, v likewise with kv_heads (slices of one projection's output are fine)
+ *   cu_seqlens  device int32 [sequences + 1], within 0 .. T
+ *   o      device bf16 [T x heads x dim], dense, written
+ *   residual  device bf16 like o, or NULL: receives the part of o that its rounding
+ *          drops, which makes the backward's gradients independent of that rounding
+ *   lse    device fp32 [heads x T], written
+ * All arrays but cu_seqlens and lse 16-byte aligned.  Scores and sums in fp32; the
+ * weights are rounded to bf16 for their product with v.  The same bits on every run.
+ * A NaN or infinity in a row of k or v may reach every row of its own sequence
+ * (never of another).
+ * Errors: QLORA_EINVAL (null pointer, size <= 0, heads % kv_heads, a pitch below
+ * its row, scale not positive and finite), QLORA_ENOTSUP (dim > 128 or not a
+ * multiple of 8, pitch not a multiple of 8 or above 2^23, T > 2^30, too many
+ * rows x heads for one launch), QLORA_EALIGN.
+ */
+int qlora_attention_fwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
+                        const qlora_bf16 *v, const int32_t *cu_seqlens, qlora_bf16 *o, qlora_bf16 *residual,
+                        float *lse, void *stream);
+
+/* Bytes of device workspace qlora_attention_bwd needs (0 for an invalid shape). */
+size_t qlora_attention_workspace(const qlora_attention_shape *shape);
+
+/*
+ * qlora_attention_bwd -- the gradients of qlora_attention_fwd: with p = e^(scale q_i k_j - lse_i),
+ *   ds_ij = scale p (do_i v_j - do_i o_i)    dq_i = sum_j ds_ij k_j
+ *   dk_j = sum_i ds_ij q_i                   dv_j = sum_i p do_i    (i over all heads of the group)
+ *   o, residual (or NULL), lse  the forward's outputs;  dout  like o
+ *   dq, dk, dv  device bf16, rows lddq, lddk, lddv elements apart (multiples of 8), written
+ *   ws  >= qlora_attention_workspace(shape) bytes.
+ */
+int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
+                        const qlora_bf16 *v, const qlora_bf16 *o, const qlora_bf16 *residual, const float *lse,
+                        const qlora_bf16 *dout, const int32_t *cu_seqlens, qlora_bf16 *dq, int64_t lddq,
+                        qlora_bf16 *dk, int64_t lddk, qlora_bf16 *dv, int64_t lddv, void *ws, size_t ws_bytes,
+                        void *stream);
+
 /* Bytes of device workspace qlora_logprob_fwd needs (0 for invalid arguments). */
 size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top);
 

@@ -1,6 +1,6 @@
 """The operators around the linear layer in a fine-tuning step, on the host in
-64 bits (numpy), from their definitions: layer norm, token log-probabilities,
-AdamW.  AdamW's states are also given in the library's stated IEEE fp32 steps
+64 bits (numpy), from their definitions: layer norm, causal attention over packed
+sequences, token log-probabilities, AdamW.  AdamW's states are also given in the library's stated IEEE fp32 steps
 (8-bit codes and scales are a bit-exact contract)."""
 from __future__ import annotations
 
@@ -31,6 +31,37 @@ def layernorm_backward(x, dy, mean, rstd, w=None):
     g = dy if w is None else dy * np.asarray(w, dtype=np.float64)
     dx = rstd * (g - g.mean(1, keepdims=True) - hat * (g * hat).mean(1, keepdims=True))
     return dx, (dy * hat).sum(0), dy.sum(0)
+
+
+def attention(q, k, v, starts, scale, dout=None):
+    """Causal attention over the sequences starts[s] .. starts[s + 1]: (o [T, H, D], lse [H, T]) and,
+    with dout, (dq, dk, dv), fp64.  Rows of no sequence: o = 0, lse = -inf, no gradient."""
+    q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
+    rows, heads, _ = q.shape
+    group = heads // k.shape[1]
+    o, lse = np.zeros_like(q), np.full((heads, rows), -np.inf)
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    for a, b in zip(starts[:-1], starts[1:]):
+        if b <= a:
+            continue
+        later = np.triu(np.ones((b - a, b - a), dtype=bool), 1)
+        for h in range(heads):
+            g = h // group
+            s = np.where(later, -np.inf, scale * q[a:b, h] @ k[a:b, g].T)
+            m = s.max(1, keepdims=True)
+            e = np.exp(s - m)
+            total = e.sum(1, keepdims=True)
+            p = e / total
+            lse[h, a:b] = (m + np.log(total))[:, 0]
+            o[a:b, h] = p @ v[a:b, g]
+            if dout is not None:
+                do = np.asarray(dout[a:b, h], dtype=np.float64)
+                dp = do @ v[a:b, g].T
+                ds = scale * p * (dp - (p * dp).sum(1, keepdims=True))
+                dq[a:b, h] = ds @ k[a:b, g]
+                dk[a:b, g] += ds.T @ q[a:b, h]
+                dv[a:b, g] += p.T @ do
+    return (o, lse) if dout is None else (o, lse, dq, dk, dv)
 
 
 def _log_softmax(row):

@@ -49,6 +49,48 @@ def test_layernorm_bwd_refusals(kw, status):
     assert norm_bwd(**kw) == status
 
 
+def attention(call="fwd", shape=None, no_shape=False, q_=FAKE, k=FAKE, v=FAKE, cu=FAKE, o=FAKE, res=None, lse=FAKE,
+              do=FAKE, dq=FAKE, dk=FAKE, dv=FAKE, lddq=512, lddk=128, lddv=128, ws=FAKE, ws_bytes=1 << 30):
+    s = dict(T=100, sequences=2, heads=8, kv_heads=2, dim=64, ldq=512, ldk=128, ldv=128, scale=0.125)
+    s.update(shape or {})
+    p = None if no_shape else ctypes.byref(q._CAttentionShape(**s))
+    if call == "fwd":
+        return q.library().qlora_attention_fwd(p, q_, k, v, cu, o, res, lse, None)
+    return q.library().qlora_attention_bwd(p, q_, k, v, o, res, lse, do, cu, dq, lddq, dk, lddk, dv, lddv, ws, ws_bytes,
+                                           None)
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd"])
+@pytest.mark.parametrize("kw,status", [
+    (dict(no_shape=True), q.QLORA_EINVAL), (dict(q_=None), q.QLORA_EINVAL), (dict(k=None), q.QLORA_EINVAL),
+    (dict(v=None), q.QLORA_EINVAL), (dict(cu=None), q.QLORA_EINVAL), (dict(o=None), q.QLORA_EINVAL),
+    (dict(lse=None), q.QLORA_EINVAL), (dict(shape=dict(T=0)), q.QLORA_EINVAL),
+    (dict(shape=dict(sequences=0)), q.QLORA_EINVAL), (dict(shape=dict(heads=7)), q.QLORA_EINVAL),
+    (dict(shape=dict(kv_heads=0)), q.QLORA_EINVAL), (dict(shape=dict(dim=-8)), q.QLORA_EINVAL),
+    (dict(shape=dict(scale=0.0)), q.QLORA_EINVAL), (dict(shape=dict(scale=float("nan"))), q.QLORA_EINVAL),
+    (dict(shape=dict(scale=float("inf"))), q.QLORA_EINVAL), (dict(shape=dict(ldq=504)), q.QLORA_EINVAL),
+    (dict(shape=dict(ldk=120)), q.QLORA_EINVAL), (dict(shape=dict(dim=60)), q.QLORA_ENOTSUP),
+    (dict(shape=dict(dim=136)), q.QLORA_ENOTSUP), (dict(shape=dict(ldv=132)), q.QLORA_ENOTSUP),
+    (dict(shape=dict(ldq=(1 << 23) + 8)), q.QLORA_ENOTSUP), (dict(shape=dict(T=(1 << 30) + 1)), q.QLORA_ENOTSUP),
+    (dict(shape=dict(T=1 << 30, heads=512, ldq=512 * 64)), q.QLORA_ENOTSUP),
+    (dict(q_=FAKE + 8), q.QLORA_EALIGN), (dict(k=FAKE + 2), q.QLORA_EALIGN), (dict(v=FAKE + 4), q.QLORA_EALIGN),
+    (dict(o=FAKE + 8), q.QLORA_EALIGN), (dict(res=FAKE + 8), q.QLORA_EALIGN), (dict(cu=FAKE + 2), q.QLORA_EALIGN),
+    (dict(lse=FAKE + 1), q.QLORA_EALIGN),
+])
+def test_attention_refusals(call, kw, status):
+    assert attention(call, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(do=None), q.QLORA_EINVAL), (dict(dq=None), q.QLORA_EINVAL), (dict(dk=None), q.QLORA_EINVAL),
+    (dict(dv=None), q.QLORA_EINVAL), (dict(lddq=504), q.QLORA_EINVAL), (dict(lddk=132), q.QLORA_ENOTSUP),
+    (dict(do=FAKE + 8), q.QLORA_EALIGN), (dict(dv=FAKE + 8), q.QLORA_EALIGN), (dict(ws=None), q.QLORA_EWORKSPACE),
+    (dict(ws_bytes=100 * 8 * 4 - 1), q.QLORA_EWORKSPACE), (dict(ws=FAKE + 8), q.QLORA_EALIGN),
+])
+def test_attention_bwd_refusals(kw, status):
+    assert attention("bwd", **kw) == status
+
+
 def lp_fwd(x=FAKE, t=0, m=4, v=100, ld=100, tg=FAKE, top=3, lp=FAKE, ent=FAKE, lse=FAKE, tl=FAKE, ti=FAKE, ws=FAKE,
            ws_bytes=1 << 30):
     return q.library().qlora_logprob_fwd(x, t, m, v, ld, tg, top, lp, ent, lse, tl, ti, ws, ws_bytes, None)
@@ -132,12 +174,16 @@ def test_workspace_sizes():
     assert q.logprob_workspace_bytes(4, 100, 17) == 0 and q.logprob_workspace_bytes(4, 100, 16) > 0
 
 
-def test_adamw_struct_layouts_match_the_header(tmp_path):
+STRUCTS = (("qlora_adamw_tensor", q._CAdamWTensor), ("qlora_adamw_config", q._CAdamWConfig),
+           ("qlora_attention_shape", q._CAttentionShape))
+
+
+def test_struct_layouts_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         pytest.skip("no host C compiler")
     body = ""
-    for name, t in (("qlora_adamw_tensor", q._CAdamWTensor), ("qlora_adamw_config", q._CAdamWConfig)):
+    for name, t in STRUCTS:
         body += f'printf("%zu\\n", sizeof({name}));\n'
         body += "".join(f'printf("%zu\\n", offsetof({name}, {f[0]}));\n' for f in t._fields_)
     src = tmp_path / "layout.c"
@@ -146,7 +192,7 @@ def test_adamw_struct_layouts_match_the_header(tmp_path):
     subprocess.run([cc, "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
     want = []
-    for t in (q._CAdamWTensor, q._CAdamWConfig):
+    for _, t in STRUCTS:
         want += [ctypes.sizeof(t)] + [getattr(t, f[0]).offset for f in t._fields_]
     assert got == want
 

@@ -30,6 +30,7 @@ int check_norm(const void *x, int32_t x_type, int64_t M, int64_t n, int64_t ldx,
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // row numbers and tile ends stay below 2^31
+constexpr float kMinScale = 0x1p-64f;             // lse / scale stays far from overflow
 constexpr int64_t kMaxPitch = int64_t(1) << 23;   // 64 rows of a tile lie within 2^30 bytes
 
 // A matrix of `width` values a row: pitch and alignment of 16-byte accesses.
@@ -42,6 +43,7 @@ int check_attention(const qlora_attention_shape *s, AttentionShape *a) {
     if (!s) return QLORA_EINVAL;
     if (s->T <= 0 || s->sequences <= 0 || s->heads <= 0 || s->kv_heads <= 0 || s->dim <= 0) return QLORA_EINVAL;
     if (s->heads % s->kv_heads != 0 || !(s->scale > 0.0f) || std::isinf(s->scale)) return QLORA_EINVAL;
+    if (s->scale < kMinScale) return QLORA_ENOTSUP;
     if (s->dim % 8 != 0 || s->dim > 128 || s->T > kMaxTokens || s->sequences > kMaxTokens) return QLORA_ENOTSUP;
     const int64_t wide = (int64_t)s->heads * s->dim, narrow = (int64_t)s->kv_heads * s->dim;
     if (wide > kMaxPitch) return QLORA_ENOTSUP;  // the dense rows of o
@@ -141,7 +143,7 @@ int qlora_attention_fwd(const qlora_attention_shape *shape, const qlora_bf16 *q,
 size_t qlora_attention_workspace(const qlora_attention_shape *shape) {
     AttentionShape a;
     if (check_attention(shape, &a) != QLORA_OK) return 0;
-    return round_up(sizeof(float) * (size_t)a.T * a.H, 256);  // delta
+    return round_up(attention_bwd_bytes(a), 256);
 }
 
 int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
@@ -166,7 +168,7 @@ int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q,
     if (!aligned(ws, 16)) return QLORA_EALIGN;
     (void)hipGetLastError();
     return hip_status(launch_attention_bwd(a, q, k, v, o, residual, lse, dout, cu_seqlens, dq, lddq, dk, lddk, dv, lddv,
-                                           static_cast<float *>(ws), static_cast<hipStream_t>(stream)));
+                                           ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top) {

@@ -26,7 +26,9 @@
 //   dk, dv   S = Q K',  dP = dO V',  dV' += dO' P, dK' += Q' dS
 // Scores, statistics, sums and gradients are fp32; P and dS are rounded to bf16
 // for their product, which the matrix cores take no wider (relative 2^-9, as
-// every stored input).  delta's o is taken with its rounding residual where the
+// every stored input).  Backward, the score products start from -lse / scale and
+// the dp products from -delta, so that their results are the exponent and the
+// second factor of ds at once.  delta's o is taken with its rounding residual where the
 // forward saved it, so that the bf16 of o does not enter dS.
 //
 // A workgroup is 4 waves with 32 rows each; the 64-row tiles of the other side
@@ -82,8 +84,8 @@ __device__ __forceinline__ bf16x8 operand_of(const f32x16 &t, int s) {
     w.w = pack_bf16x2(t[8 * s + 6], t[8 * s + 7]);
     return __builtin_bit_cast(bf16x8, w);
 }
-// The row of an accumulator tile that register i holds in half h of the wave.
-__device__ __forceinline__ int tile_row(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
+// The row of an accumulator tile that register i holds in the wave's lower half; the upper half's is 4 further.
+__device__ __forceinline__ constexpr int tile_row(int i) { return (i & 3) + 8 * (i >> 2); }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float pair_max(float v) {
@@ -135,69 +137,87 @@ __device__ __forceinline__ int swizzle(int r) {
     return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
 }
 
-// 16 bytes a lane from global memory to LDS: lane l writes dst + 16 l.
-__device__ __forceinline__ void transfer16(__amdgpu_buffer_rsrc_t r, const void *dst, uint32_t voff) {
+// 16 (or 4) bytes a lane from global memory to LDS: lane l writes dst + 16 l (4 l).
+__device__ __forceinline__ void transfer16(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, reinterpret_cast<__attribute__((address_space(3))) void *>(reinterpret_cast<uintptr_t>(dst)), 16, voff, 0, 0,
-        0);
+        r, reinterpret_cast<__attribute__((address_space(3))) void *>(dst), 16, voff, 0, 0, 0);
+}
+__device__ __forceinline__ void transfer4(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, reinterpret_cast<__attribute__((address_space(3))) void *>(dst), 4, voff, 0, 0, 0);
 }
 
-// The transfers of a wave: its quarter of a 64-row tile.
-template <int DP>
+// The transfers of a wave: its quarter of a tile of ROWS rows, kRows at a time.
+// The chunk that a lane brings differs between its rows by an exclusive or with
+// the row group's number.  KEEP: the offsets stay in registers over the kernel;
+// otherwise two registers hold them and they are formed at every tile, for a
+// kernel that has no registers left.
+template <int DP, int ROWS, bool KEEP>
 struct Mover {
-    static constexpr int kChunks = DP / 8, kRows = 64 / kChunks, kOps = kStream / kWaves / kRows;
-    uint32_t voff[kOps];
+    static constexpr int kChunks = DP / 8, kRows = 64 / kChunks, kOwnRows = ROWS / kWaves, kOps = kOwnRows / kRows;
+    uint32_t base, chunk, off[KEEP ? kOps : 1];
+    __device__ __forceinline__ uint32_t offset(uint32_t base, uint32_t chunk, int64_t ld, int D, int i) const {
+        const uint32_t c = chunk ^ swizzle<DP>(i * kRows);
+        // columns past D lie past every range
+        return c * 8 < (uint32_t)D ? base + (uint32_t)(i * kRows * ld * 2) + c * 16 : 0x80000000u;
+    }
     __device__ __forceinline__ void init(int64_t ld, int D) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int lane = threadIdx.x & 63, row = (threadIdx.x >> 6) * kOwnRows + lane / kChunks;
+        base = (uint32_t)(row * ld * 2);
+        chunk = (lane % kChunks) ^ swizzle<DP>(row);
+        if (KEEP) {
 #pragma unroll
-        for (int i = 0; i < kOps; ++i) {
-            const int row = wave * (kStream / kWaves) + i * kRows + lane / kChunks;
-            const int c = (lane % kChunks) ^ swizzle<DP>(row);
-            // columns past D lie past every range: zeros
-            voff[i] = c * 8 < D ? (uint32_t)(row * ld * 2 + c * 16) : 0x80000000u;
+            for (int i = 0; i < kOps; ++i) off[i] = offset(base, chunk, ld, D, i);
         }
     }
-    // Rows [row0, row0 + 64) of x (pitch ld) to dst; zeros from row `end` on.
-    __device__ __forceinline__ void load(const uint16_t *x, int64_t ld, int row0, int end, uint16_t *dst) const {
+    // Rows [row0, row0 + ROWS) of x (pitch ld) to dst; zeros from row `end` and column D on.
+    __device__ __forceinline__ void load(const uint16_t *x, int64_t ld, int D, int row0, int end, uint32_t dst) const {
         int rows = end - row0;
-        rows = rows < 0 ? 0 : rows > kStream ? kStream : rows;
+        rows = rows < 0 ? 0 : rows > ROWS ? ROWS : rows;
         const __amdgpu_buffer_rsrc_t r = out_rsrc(x + (int64_t)row0 * ld, (int64_t)rows * ld * 2);
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        uint32_t b = base, ch = chunk;
+        if (!KEEP) asm volatile("" : "+v"(b), "+v"(ch));  // formed here, not kept over the kernel's loop
 #pragma unroll
-        for (int i = 0; i < kOps; ++i) {
-            const uint16_t *at = dst + (wave * (kStream / kWaves) + i * kRows) * DP;
-            transfer16(r, at, voff[i]);
-        }
+        for (int i = 0; i < kOps; ++i)
+            transfer16(r, dst + (wave * kOwnRows + i * kRows) * DP * 2,
+                       KEEP ? off[KEEP ? i : 0] : offset(b, ch, ld, D, i));
     }
 };
 
-// Addresses inside a tile of what a lane reads: row fragments (32 rows, 16
-// columns: row l % 32, columns 16 ks + 8 (l / 32) ..) and transposed fragments
-// (32 columns from 32 dt, rows 16 s + 4 (l / 32) .. and 8 further).
-template <int DP>
+// What a lane reads of a tile: row fragments (32 rows, 16 columns: row l % 32,
+// columns 16 ks + 8 (l / 32) ..) and transposed fragments (32 columns from 32
+// dt, rows 16 s + 4 (l / 32) .. and 8 further).  The chunk order is an exclusive
+// or, so every step's address is the lane's first one with a constant xored in
+// (tiles start at multiples of their row size).  KEEP: the steps' addresses stay
+// in registers, with the tile and the rows as the instructions' offsets.
+template <int DP, bool KEEP>
 struct Reader {
-    static constexpr int kSteps = DP / 16, kTiles = DP / 32;
-    uint32_t row[kSteps], col[kTiles][2];
+    static constexpr int kSteps = DP / 16, kTiles = DP / 32, kRow = DP * 2;
+    uint32_t row0, col0, row[KEEP ? kSteps : 1], col[KEEP ? kSteps : 1];
     __device__ __forceinline__ void init() {
         const int l = threadIdx.x & 63, h = l >> 5, r = l & 31, i = l & 15, g = (l >> 4) & 1;
+        row0 = r * kRow + (h ^ swizzle<DP>(r)) * 16;
+        const int rr = 4 * h + i / 4;
+        col0 = rr * kRow + ((g * 2 + (i & 3) / 2) ^ swizzle<DP>(rr)) * 16 + (i & 1) * 8;
+        if (KEEP) {
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) row[ks] = r * DP * 2 + (((2 * ks + h) ^ swizzle<DP>(r)) * 16);
-#pragma unroll
-        for (int dt = 0; dt < kTiles; ++dt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int rr = 8 * u + 4 * h + i / 4, c = dt * 4 + g * 2 + (i & 3) / 2;
-                col[dt][u] = rr * DP * 2 + ((c ^ swizzle<DP>(rr)) * 16) + (i & 1) * 8;
+            for (int ks = 0; ks < kSteps; ++ks) {
+                row[ks] = row0 ^ (ks * 32);
+                col[ks] = col0 ^ (ks * 32);
             }
+        }
     }
     // Rows 32 kt .. 32 kt + 31, column step ks.
     __device__ __forceinline__ bf16x8 rows(uint32_t tile, int kt, int ks) const {
-        return lds_frag(tile + row[ks] + kt * 32 * DP * 2);
+        const uint32_t at = KEEP ? row[KEEP ? ks : 0] + tile : (tile + row0) ^ (ks * 32);
+        return lds_frag(at + kt * 32 * kRow);
     }
     // Columns 32 dt .., row step s (rows 16 s .. 16 s + 15, in the accumulators' order).
     __device__ __forceinline__ bf16x8 cols(uint32_t tile, int dt, int s) const {
-        return join(lds_transposed(tile + col[dt][0] + s * 16 * DP * 2),
-                    lds_transposed(tile + col[dt][1] + s * 16 * DP * 2));
+        const uint32_t a = KEEP ? col[KEEP ? 2 * dt : 0] + tile : (tile + col0) ^ (dt * 64);
+        const uint32_t b = KEEP ? col[KEEP ? 2 * dt + 1 : 0] + tile : (tile + col0) ^ (dt * 64 + 32);
+        return join(lds_transposed(a + s * 16 * kRow), lds_transposed(b + s * 16 * kRow + 8 * kRow));
     }
 };
 
@@ -214,7 +234,7 @@ __device__ __forceinline__ void load_rows(const uint16_t *x, int64_t ld, int row
     }
 }
 
-// Stores a transposed result (columns 32 dt + tile_row, row l % 32) times f as bf16 rows; res: the residuals.
+// Stores a transposed result (columns 32 dt + tile_row + 4 (l / 32), row l % 32) times f as bf16 rows; res: the residuals.
 template <int DP>
 __device__ __forceinline__ void store_rows(uint16_t *y, uint16_t *res, int64_t ld, int row0, int end, int D,
                                            const f32x16 *t, float f) {
@@ -224,7 +244,7 @@ __device__ __forceinline__ void store_rows(uint16_t *y, uint16_t *res, int64_t l
     for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const int c = 32 * dt + tile_row(i, h);
+            const int c = 32 * dt + tile_row(i) + 4 * h;
             if (c >= D) continue;
             const float a = t[dt][i] * f, b = t[dt][i + 1] * f, d = t[dt][i + 2] * f, e = t[dt][i + 3] * f;
             const uint2 w = make_uint2(pack_bf16x2(a, b), pack_bf16x2(d, e));
@@ -252,13 +272,13 @@ __device__ __forceinline__ void zero_rows(uint16_t *y, int64_t ld, int row0, int
 __device__ __forceinline__ int head_of(int p, int H, int Hk) { return (p % Hk) * (H / Hk) + p / Hk; }
 
 template <int DP>
-__global__ __launch_bounds__(kThreads) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
+__global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
                                                                  const uint16_t *__restrict__ k,
                                                                  const uint16_t *__restrict__ v,
                                                                  const int32_t *__restrict__ cu,
                                                                  uint16_t *__restrict__ o, uint16_t *__restrict__ res,
                                                                  float *__restrict__ lse, int slots) {
-    __shared__ __attribute__((aligned(16))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
+    __shared__ __attribute__((aligned(256))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     // the long rows' tiles first
     const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
@@ -273,10 +293,10 @@ __global__ __launch_bounds__(kThreads) void attention_fwd_kernel(AttentionShape 
     }
     const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP> mk, mv;
+    Mover<DP, kStream, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
-    Reader<DP> rd;
+    Reader<DP, true> rd;
     rd.init();
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     bf16x8 qf[DP / 16];
@@ -289,17 +309,19 @@ __global__ __launch_bounds__(kThreads) void attention_fwd_kernel(AttentionShape 
     float m = -INFINITY, sum = 0.0f;
     const float c = a.scale * kLog2e;
     const int tiles = (last - at.begin + kStream - 1) / kStream;
-    mk.load(kh, a.ldk, at.begin, at.end, ks_[0]);
-    mv.load(vh, a.ldv, at.begin, at.end, vs_[0]);
-    for (int j = 0; j < tiles; ++j) {
+    mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
+    mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
+    // B: the buffer that tile j is in, a constant so that it is part of the instructions' offsets
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
         __syncthreads();  // tile j is in LDS, and nobody reads the other buffer
         const int key0 = at.begin + j * kStream;
         if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, key0 + kStream, at.end, ks_[(j + 1) & 1]);
-            mv.load(vh, a.ldv, key0 + kStream, at.end, vs_[(j + 1) & 1]);
+            mk.load(kh, a.ldk, a.D, key0 + kStream, at.end, lds_addr(ks_[1 - B]));
+            mv.load(vh, a.ldv, a.D, key0 + kStream, at.end, lds_addr(vs_[1 - B]));
         }
-        if (key0 > row0 + 31) continue;  // the wave's rows all come before this tile
-        const uint32_t kt_ = lds_addr(ks_[j & 1]), vt_ = lds_addr(vs_[j & 1]);
+        if (key0 > row0 + 31) return;  // the wave's rows all come before this tile
+        const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
         f32x16 s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -313,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void attention_fwd_kernel(AttentionShape 
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (key0 + 32 * t + tile_row(i, h) > row) s[t][i] = -INFINITY;
+                    if (key0 + 32 * t + tile_row(i) > row - 4 * h) s[t][i] = -INFINITY;
         }
         float top = s[0][0];
 #pragma unroll
@@ -347,20 +369,24 @@ __global__ __launch_bounds__(kThreads) void attention_fwd_kernel(AttentionShape 
 #pragma unroll
             for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(vt_, dt, st), p, acc[dt]);
         }
+    };
+    for (int j = 0; j < tiles; j += 2) {
+        tile_step(j, std::integral_constant<int, 0>());
+        if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     sum = pair_sum(sum);
     store_rows<DP>(o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
     if (h == 0 && row < at.end) lse[(int64_t)head * a.T + row] = m * a.scale + logf(sum);
 }
 
-// dq, and delta for the dk, dv kernel.
+// dq, and the rows' statistics for the dk, dv kernel.
 template <int DP>
-__global__ __launch_bounds__(kThreads) void attention_dq_kernel(
+__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
     const uint16_t *__restrict__ o, const uint16_t *__restrict__ res, const float *__restrict__ lse,
     const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, uint16_t *__restrict__ dq, int64_t lddq,
-    float *__restrict__ delta, int slots) {
-    __shared__ __attribute__((aligned(16))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
+    float *__restrict__ stats, int slots) {
+    __shared__ __attribute__((aligned(256))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
@@ -372,15 +398,15 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(
     }
     const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP> mk, mv;
+    Mover<DP, kStream, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
-    Reader<DP> rd;
+    Reader<DP, true> rd;
     rd.init();
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     const int tiles = (last - at.begin + kStream - 1) / kStream;
-    mk.load(kh, a.ldk, at.begin, at.end, ks_[0]);
-    mv.load(vh, a.ldv, at.begin, at.end, vs_[0]);
+    mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
+    mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
     bf16x8 qf[DP / 16], df[DP / 16];
     load_rows<DP>(q + (int64_t)head * a.D, a.ldq, row0, at.end, a.D, qf);
     load_rows<DP>(dout + (int64_t)head * a.D, ldo, row0, at.end, a.D, df);
@@ -401,29 +427,37 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(
         }
     }
     dl = pair_sum(dl);
-    const float ls = row < at.end ? lse[(int64_t)head * a.T + row] * kLog2e : INFINITY;
-    if (h == 0 && row < at.end) delta[(int64_t)head * a.T + row] = dl;
+    dl = -dl;
+    const float ls = row < at.end ? -lse[(int64_t)head * a.T + row] / a.scale : 0.0f;
+    if (h == 0 && row < at.end) {  // the same starting values for the dk, dv kernel
+        stats[(int64_t)head * a.T + row] = ls;
+        stats[(int64_t)(a.H + head) * a.T + row] = dl;
+    }
     f32x16 acc[DP / 32];
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
     const float c = a.scale * kLog2e;
-    for (int j = 0; j < tiles; ++j) {
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
         __syncthreads();
         const int key0 = at.begin + j * kStream;
         if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, key0 + kStream, at.end, ks_[(j + 1) & 1]);
-            mv.load(vh, a.ldv, key0 + kStream, at.end, vs_[(j + 1) & 1]);
+            mk.load(kh, a.ldk, a.D, key0 + kStream, at.end, lds_addr(ks_[1 - B]));
+            mv.load(vh, a.ldv, a.D, key0 + kStream, at.end, lds_addr(vs_[1 - B]));
         }
-        const uint32_t kt_ = lds_addr(ks_[j & 1]), vt_ = lds_addr(vs_[j & 1]);
+        const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int k0 = key0 + 32 * t;
             if (k0 > row0 + 31) break;
             f32x16 s, dp;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+            for (int i = 0; i < 16; ++i) {
+                s[i] = ls;
+                dp[i] = dl;
+            }
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) {
                 s = mfma(rd.rows(kt_, t, ks), qf[ks], s);
@@ -432,9 +466,9 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(
             const bool edge = k0 + 31 > row0;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ls));
-                if (edge && k0 + tile_row(i, h) > row) p = 0.0f;
-                s[i] = p * (dp[i] - dl);
+                float p = __builtin_amdgcn_exp2f(s[i] * c);
+                if (edge && k0 + tile_row(i) > row - 4 * h) p = 0.0f;
+                s[i] = p * dp[i];
             }
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
@@ -443,37 +477,93 @@ __global__ __launch_bounds__(kThreads) void attention_dq_kernel(
                 for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(kt_, dt, 2 * t + st), ds, acc[dt]);
             }
         }
+    };
+    for (int j = 0; j < tiles; j += 2) {
+        tile_step(j, std::integral_constant<int, 0>());
+        if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     store_rows<DP>(dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
 }
 
-// dk and dv of 128 keys of one key-value head: all rows after them, all heads of the group.
+// Where the dk, dv kernel's results go: the gradients, or with `part` one fp32
+// partial a head ([2][H][T][D]: dk, dv) for the kernel that adds a group's heads.
+struct KvOut {
+    uint16_t *dk, *dv;
+    int64_t lddk, lddv;
+    float *part;
+};
+
+// Stores a transposed result times f as fp32 rows.
 template <int DP>
-__global__ __launch_bounds__(kThreads) void attention_dkv_kernel(
+__device__ __forceinline__ void store_rows_f32(float *y, int64_t ld, int row0, int end, int D, const f32x16 *t, float f) {
+    const int l = threadIdx.x & 63, h = l >> 5, row = row0 + (l & 31);
+    if (row >= end) return;
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int c = 32 * dt + tile_row(i) + 4 * h;
+            if (c < D)
+                *reinterpret_cast<f32x4 *>(y + (int64_t)row * ld + c) =
+                    f32x4{t[dt][i] * f, t[dt][i + 1] * f, t[dt][i + 2] * f, t[dt][i + 3] * f};
+        }
+}
+
+// dk and dv of 128 keys: all rows after them, of one head (SPLIT: a workgroup a
+// head, partial results) or of all heads of the group.  The keys stay in LDS and
+// the values in registers: with both in registers the two accumulators leave no
+// room for two waves a SIMD.
+template <int DP, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
-    const float *__restrict__ lse, const float *__restrict__ delta, const uint16_t *__restrict__ dout,
-    const int32_t *__restrict__ cu, uint16_t *__restrict__ dk, int64_t lddk, uint16_t *__restrict__ dv, int64_t lddv) {
-    __shared__ __attribute__((aligned(16))) uint16_t qs_[2][kStream * DP], ds_[2][kStream * DP];
-    __shared__ __attribute__((aligned(16))) float ls_[2][kStream], dl_[2][kStream];
-    const int kv = blockIdx.x % a.Hk, group = a.H / a.Hk;
-    const Place at = place_of(cu, a.S, a.T, (int)(blockIdx.x / a.Hk));  // the first keys have the most rows
+    const float *__restrict__ stats, const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, KvOut out) {
+    constexpr int kTile = 32;
+    __shared__ __attribute__((aligned(256))) uint16_t ks_[kOwn * DP], qs_[2][kTile * DP], ds_[2][kTile * DP];
+    __shared__ __attribute__((aligned(16))) float ls_[2][kTile], dl_[2][kTile];
+    const int group = a.H / a.Hk, heads = SPLIT ? a.H : a.Hk;
+    const int first_head = SPLIT ? head_of(blockIdx.x % a.H, a.H, a.Hk) : (int)(blockIdx.x % a.Hk) * group;
+    const int kv = first_head / group;
+    const Place at = place_of(cu, a.S, a.T, (int)(blockIdx.x / heads));  // the first keys have the most rows
     if (at.first >= at.end) return;
     const int64_t ldo = (int64_t)a.H * a.D;
+    float *pk = SPLIT ? out.part + (int64_t)first_head * a.T * a.D : nullptr;
+    float *pv = SPLIT ? out.part + ((int64_t)a.H + first_head) * a.T * a.D : nullptr;
     if (at.outside) {
         const int last = at.first + kOwn < at.end ? at.first + kOwn : at.end;
-        zero_rows(dk + kv * a.D, lddk, at.first, last, a.D);
-        zero_rows(dv + kv * a.D, lddv, at.first, last, a.D);
+        if (SPLIT) {
+            zero_rows(reinterpret_cast<uint16_t *>(pk), 2 * a.D, at.first, last, 2 * a.D);
+            zero_rows(reinterpret_cast<uint16_t *>(pv), 2 * a.D, at.first, last, 2 * a.D);
+        } else {
+            zero_rows(out.dk + kv * a.D, out.lddk, at.first, last, a.D);
+            zero_rows(out.dv + kv * a.D, out.lddv, at.first, last, a.D);
+        }
         return;
     }
     const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int key0 = at.first + 32 * wave, key = key0 + (l & 31);
-    Mover<DP> mq, md;
+    Mover<DP, kTile, true> mq, md;
     mq.init(a.ldq, a.D);
     md.init(ldo, a.D);
-    Reader<DP> rd;
+    Reader<DP, true> rd;
     rd.init();
-    bf16x8 kf[DP / 16], vf[DP / 16];
-    load_rows<DP>(k + (int64_t)kv * a.D, a.ldk, key0, at.end, a.D, kf);
+    // A tile of rows and their statistics.  Rows past the end are zeros throughout: p = 1
+    // there, against do = 0 and q = 0.
+    auto fetch = [&](int hd, int r0, int b) {
+        mq.load(q + (int64_t)hd * a.D, a.ldq, a.D, r0, at.end, lds_addr(qs_[b]));
+        md.load(dout + (int64_t)hd * a.D, ldo, a.D, r0, at.end, lds_addr(ds_[b]));
+        if (wave < 2 && l < kTile) {
+            const __amdgpu_buffer_rsrc_t r = out_rsrc(stats + (int64_t)(wave * a.H + hd) * a.T + r0, (int64_t)(at.end - r0) * 4);
+            transfer4(r, lds_addr(wave ? dl_[b] : ls_[b]), l * 4);
+        }
+    };
+    int hd = first_head, r0 = at.first;  // of the tile at hand
+    {
+        Mover<DP, kOwn, false> mk;
+        mk.init(a.ldk, a.D);
+        mk.load(k + (int64_t)kv * a.D, a.ldk, a.D, at.first, at.end, lds_addr(ks_));
+    }
+    fetch(hd, r0, 0);
+    bf16x8 vf[DP / 16];
     load_rows<DP>(v + (int64_t)kv * a.D, a.ldv, key0, at.end, a.D, vf);
     f32x16 ak[DP / 32], av[DP / 32];
 #pragma unroll
@@ -481,71 +571,128 @@ __global__ __launch_bounds__(kThreads) void attention_dkv_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.0f;
     const float c = a.scale * kLog2e;
-    const int per = (at.end - at.first + kStream - 1) / kStream, tiles = per * group;  // tiles of rows, head by head
-    auto fetch = [&](int j) {
-        const int hd = kv * group + j / per, r0 = at.first + (j % per) * kStream, b = j & 1;
-        mq.load(q + (int64_t)hd * a.D, a.ldq, r0, at.end, qs_[b]);
-        md.load(dout + (int64_t)hd * a.D, ldo, r0, at.end, ds_[b]);
-        if (threadIdx.x < kStream) {  // a row past the end has lse = inf: p = 0
-            const int r = r0 + threadIdx.x;
-            const bool in = r < at.end;
-            ls_[b][threadIdx.x] = in ? lse[(int64_t)hd * a.T + r] * kLog2e : INFINITY;
-            dl_[b][threadIdx.x] = in ? delta[(int64_t)hd * a.T + r] : 0.0f;
+    uint32_t kt_ = lds_addr(ks_) + 32 * wave * DP * 2;
+    const int per = (at.end - at.first + kTile - 1) / kTile, tiles = per * (SPLIT ? 1 : group);
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
+        __syncthreads();
+        int next_hd = hd, next_r0 = r0 + kTile;
+        if (next_r0 >= at.end) {
+            ++next_hd;
+            next_r0 = at.first;
+        }
+        if (j + 1 < tiles) fetch(next_hd, next_r0, 1 - B);
+        const uint32_t qt_ = lds_addr(qs_[B]), dt_ = lds_addr(ds_[B]);
+        const uint32_t lt_ = lds_addr(ls_[B]) + 16 * h, et_ = lds_addr(dl_[B]) + 16 * h;
+        const int q0 = r0;
+        hd = next_hd;
+        r0 = next_r0;
+        if (q0 + 31 < key0) return;  // these rows all come before the wave's keys
+        asm volatile("" : "+s"(kt_));  // read the keys again, do not keep their fragments over the loop
+        f32x16 s, dp;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const f32x4 ls = *reinterpret_cast<const lds_f32x4 *>(lt_ + 2 * i * 4);
+            const f32x4 dl = *reinterpret_cast<const lds_f32x4 *>(et_ + 2 * i * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[i + e] = ls[e];
+                dp[i + e] = dl[e];
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            s = mfma(rd.rows(qt_, 0, ks), rd.rows(kt_, 0, ks), s);
+            dp = mfma(rd.rows(dt_, 0, ks), vf[ks], dp);
+        }
+        const bool edge = q0 < key0 + 31;
+        u32x4 pw[2], sw[2];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            float p0 = __builtin_amdgcn_exp2f(s[i] * c), p1 = __builtin_amdgcn_exp2f(s[i + 1] * c);
+            if (edge && q0 + tile_row(i) < key - 4 * h) p0 = 0.0f;
+            if (edge && q0 + tile_row(i + 1) < key - 4 * h) p1 = 0.0f;
+            pw[i / 8][i / 2 % 4] = pack_bf16x2(p0, p1);
+            sw[i / 8][i / 2 % 4] = pack_bf16x2(p0 * dp[i], p1 * dp[i + 1]);
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const bf16x8 pb = __builtin_bit_cast(bf16x8, pw[st]), sb = __builtin_bit_cast(bf16x8, sw[st]);
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; ++dt) {
+                av[dt] = mfma(rd.cols(dt_, dt, st), pb, av[dt]);
+                ak[dt] = mfma(rd.cols(qt_, dt, st), sb, ak[dt]);
+            }
         }
     };
-    fetch(0);
-    for (int j = 0; j < tiles; ++j) {
-        __syncthreads();
-        if (j + 1 < tiles) fetch(j + 1);
-        const int r0 = at.first + (j % per) * kStream;
-        const uint32_t qt_ = lds_addr(qs_[j & 1]), dt_ = lds_addr(ds_[j & 1]);
-        const uint32_t lt_ = lds_addr(ls_[j & 1]) + 16 * h, et_ = lds_addr(dl_[j & 1]) + 16 * h;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int q0 = r0 + 32 * t;
-            if (q0 + 31 < key0) continue;  // these rows all come before the wave's keys
-            f32x16 s, dp;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-                s = mfma(rd.rows(qt_, t, ks), kf[ks], s);
-                dp = mfma(rd.rows(dt_, t, ks), vf[ks], dp);
-            }
-            const bool edge = q0 < key0 + 31;
-            f32x16 p;
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const f32x4 ls = *reinterpret_cast<const lds_f32x4 *>(lt_ + (32 * t + 2 * i) * 4);
-                const f32x4 dl = *reinterpret_cast<const lds_f32x4 *>(et_ + (32 * t + 2 * i) * 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float pe = __builtin_amdgcn_exp2f(fmaf(s[i + e], c, -ls[e]));
-                    if (edge && q0 + tile_row(i + e, h) < key) pe = 0.0f;
-                    p[i + e] = pe;
-                    s[i + e] = pe * (dp[i + e] - dl[e]);
-                }
-            }
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const bf16x8 pb = operand_of(p, st), sb = operand_of(s, st);
-#pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt) {
-                    av[dt] = mfma(rd.cols(dt_, dt, 2 * t + st), pb, av[dt]);
-                    ak[dt] = mfma(rd.cols(qt_, dt, 2 * t + st), sb, ak[dt]);
-                }
-            }
-        }
+    for (int j = 0; j < tiles; j += 2) {
+        tile_step(j, std::integral_constant<int, 0>());
+        if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
-    store_rows<DP>(dk + kv * a.D, nullptr, lddk, key0, at.end, a.D, ak, a.scale);
-    store_rows<DP>(dv + kv * a.D, nullptr, lddv, key0, at.end, a.D, av, 1.0f);
+    if (SPLIT) {
+        store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
+        store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
+    } else {
+        store_rows<DP>(out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
+        store_rows<DP>(out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
+    }
+}
+
+// dk (blockIdx.y 0) and dv (1) from the heads' partials, added in head order.
+__global__ __launch_bounds__(kThreads) void attention_group_sum_kernel(AttentionShape a, KvOut out) {
+    const int chunks = a.D / 8;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, n = (int64_t)a.T * a.Hk * chunks;
+    if (i >= n) return;
+    const int64_t row = i / (a.Hk * chunks);
+    const int kv = (int)(i / chunks % a.Hk), c = (int)(i % chunks) * 8, group = a.H / a.Hk;
+    const float *p = out.part + (((int64_t)blockIdx.y * a.H + kv * group) * a.T + row) * a.D + c;
+    f32x4 lo = {}, hi = {};
+    for (int g = 0; g < group; ++g, p += (int64_t)a.T * a.D) {
+        lo += *reinterpret_cast<const f32x4 *>(p);
+        hi += *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    uint16_t *y = (blockIdx.y ? out.dv + row * out.lddv : out.dk + row * out.lddk) + kv * a.D + c;
+    *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
+                                               pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
 }
 
 int slots_of(const AttentionShape &a) { return a.T / kOwn + a.S + 2; }
 
+// A workgroup a head instead of a group in the dk, dv kernel: where the groups'
+// tiles would give each CU less than two rounds of its two workgroups, and the
+// longest of them, the first keys of a sequence with all heads' rows, would run
+// alone at the end.
+bool split_heads(const AttentionShape &a) { return a.H > a.Hk && (int64_t)(a.T / kOwn) * a.Hk < 1024; }
+size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
+
+template <int DP>
+hipError_t backward(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                    const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout, const int32_t *cu,
+                    uint16_t *dq, int64_t lddq, float *stats, const KvOut &out, hipStream_t s) {
+    const int slots = slots_of(a);
+    attention_dq_kernel<DP><<<(unsigned)slots * a.H, kThreads, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats,
+                                                                      slots);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (!split_heads(a)) {
+        attention_dkv_kernel<DP, false><<<(unsigned)slots * a.Hk, kThreads, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+        return hipGetLastError();
+    }
+    attention_dkv_kernel<DP, true><<<(unsigned)slots * a.H, kThreads, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t chunks = (int64_t)a.T * a.Hk * (a.D / 8);
+    attention_group_sum_kernel<<<dim3((unsigned)((chunks + kThreads - 1) / kThreads), 2), kThreads, 0, s>>>(a, out);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t attention_groups(const AttentionShape &a) { return (int64_t)slots_of(a) * a.H; }
+
+size_t attention_bwd_bytes(const AttentionShape &a) {
+    return stats_bytes(a) + (split_heads(a) ? sizeof(float) * 2 * (size_t)a.T * a.H * a.D : 0);
+}
 
 hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s) {
@@ -561,20 +708,11 @@ hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, cons
 hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout,
                                 const int32_t *cu, uint16_t *dq, int64_t lddq, uint16_t *dk, int64_t lddk,
-                                uint16_t *dv, int64_t lddv, float *delta, hipStream_t s) {
-    const int slots = slots_of(a);
-    const unsigned gq = (unsigned)slots * a.H, gk = (unsigned)slots * a.Hk;
-    if (a.D <= 64)
-        attention_dq_kernel<64><<<gq, kThreads, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, delta, slots);
-    else
-        attention_dq_kernel<128><<<gq, kThreads, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, delta, slots);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.D <= 64)
-        attention_dkv_kernel<64><<<gk, kThreads, 0, s>>>(a, q, k, v, lse, delta, dout, cu, dk, lddk, dv, lddv);
-    else
-        attention_dkv_kernel<128><<<gk, kThreads, 0, s>>>(a, q, k, v, lse, delta, dout, cu, dk, lddk, dv, lddv);
-    return hipGetLastError();
+                                uint16_t *dv, int64_t lddv, void *ws, hipStream_t s) {
+    float *stats = static_cast<float *>(ws);
+    const KvOut out{dk, dv, lddk, lddv, reinterpret_cast<float *>(static_cast<char *>(ws) + stats_bytes(a))};
+    return a.D <= 64 ? backward<64>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s)
+                     : backward<128>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
 }
 
 }  // namespace qnf4

@@ -230,12 +230,14 @@ struct AttentionShape {
     float scale;
 };
 int64_t attention_groups(const AttentionShape &a);  // workgroups of the largest launch
-// cu: S + 1 starts on the device; o, res, dout dense [T x H x D] (res may be null); lse, delta [H x T].
+size_t attention_bwd_bytes(const AttentionShape &a);
+// cu: S + 1 starts on the device; o, res, dout dense [T x H x D] (res may be null); lse [H x T];
+// ws: attention_bwd_bytes(a), 16-byte aligned.
 hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s);
 hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout,
                                 const int32_t *cu, uint16_t *dq, int64_t lddq, uint16_t *dk, int64_t lddk,
-                                uint16_t *dv, int64_t lddv, float *delta, hipStream_t s);
+                                uint16_t *dv, int64_t lddv, void *ws, hipStream_t s);
 
 }  // namespace qnf4

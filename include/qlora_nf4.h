@@ -449,7 +449,7 @@ typedef struct {
  * (never of another).
  * Errors: QLORA_EINVAL (null pointer, size <= 0, heads % kv_heads, a pitch below
  * its row, scale not positive and finite), QLORA_ENOTSUP (dim > 128 or not a
- * multiple of 8, pitch not a multiple of 8 or above 2^23, T > 2^30, too many
+ * multiple of 8, scale < 2^-64, pitch not a multiple of 8 or above 2^23, T > 2^30, too many
  * rows x heads for one launch), QLORA_EALIGN.
  */
 int qlora_attention_fwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,

@@ -69,6 +69,7 @@ def attention(call="fwd", shape=None, no_shape=False, q_=FAKE, k=FAKE, v=FAKE, c
     (dict(shape=dict(kv_heads=0)), q.QLORA_EINVAL), (dict(shape=dict(dim=-8)), q.QLORA_EINVAL),
     (dict(shape=dict(scale=0.0)), q.QLORA_EINVAL), (dict(shape=dict(scale=float("nan"))), q.QLORA_EINVAL),
     (dict(shape=dict(scale=float("inf"))), q.QLORA_EINVAL), (dict(shape=dict(ldq=504)), q.QLORA_EINVAL),
+    (dict(shape=dict(scale=1e-20)), q.QLORA_ENOTSUP),
     (dict(shape=dict(ldk=120)), q.QLORA_EINVAL), (dict(shape=dict(dim=60)), q.QLORA_ENOTSUP),
     (dict(shape=dict(dim=136)), q.QLORA_ENOTSUP), (dict(shape=dict(ldv=132)), q.QLORA_ENOTSUP),
     (dict(shape=dict(ldq=(1 << 23) + 8)), q.QLORA_ENOTSUP), (dict(shape=dict(T=(1 << 30) + 1)), q.QLORA_ENOTSUP),

@@ -112,20 +112,20 @@ __device__ __forceinline__ int bound_at(const int32_t *cu, int S, int T, int i) 
 }
 __device__ __forceinline__ Place place_of(const int32_t *cu, int S, int T, int slot) {
     const int lane = threadIdx.x & 63;
-    int lo = 0, len = S + 2;
-    while (len > 1) {
-        const int step = (len + 63) / 64, i = lo + lane * step;
-        const bool before = lane * step < len && bound_at(cu, S, T, i) / kOwn + i <= slot;
-        int n = __popcll(__ballot(before));
-        n = n < 1 ? 1 : n;
+    int lo = 0, len = S + 2, n, bound, step;
+    do {
+        step = (len + 63) / 64;
+        const int i = lo + lane * step;
+        bound = bound_at(cu, S, T, i);
+        n = __popcll(__ballot(lane * step < len && bound / kOwn + i <= slot));
+        n = __builtin_amdgcn_readfirstlane(n < 1 ? 1 : n);
         const int left = len - (n - 1) * step;
         lo += (n - 1) * step;
         len = step < left ? step : left;
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    Place p;
-    p.begin = __builtin_amdgcn_readfirstlane(bound_at(cu, S, T, lo));
-    p.end = __builtin_amdgcn_readfirstlane(bound_at(cu, S, T, lo + 1));
+    } while (step > 1);
+    Place p;  // the last step's lanes hold the segments' starts one by one
+    p.begin = __builtin_amdgcn_readlane(bound, n - 1);
+    p.end = n < 64 ? __builtin_amdgcn_readlane(bound, n) : __builtin_amdgcn_readfirstlane(bound_at(cu, S, T, lo + 1));
     p.first = p.begin + (slot - (p.begin / kOwn + lo)) * kOwn;
     p.outside = lo == 0 || lo == S + 1;
     return p;

@@ -173,7 +173,7 @@ int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q,
 
 size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top) {
     if (M <= 0 || V <= 0 || V > kMaxVocab || M > kMaxRows || top < 0 || top > kMaxTop) return 0;
-    return round_up(logprob_stats_bytes(M, V), 256) + round_up(logprob_best_bytes(M, V, top), 256);
+    return 16 + round_up(logprob_stats_bytes(M, V), 256) + round_up(logprob_best_bytes(M, V, top), 256);
 }
 
 int qlora_logprob_fwd(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld, const int64_t *targets,

@@ -42,6 +42,63 @@ __device__ __forceinline__ F8 load8(const float *p) {
 __device__ __forceinline__ float load1(const uint16_t *p) { return bf16_bits_to_f32(*p); }
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 
+// A group as it is in memory: its load can be under way while others are issued.
+struct Raw16 {
+    u32x4 w;
+};
+struct Raw32 {
+    u32x4 w[2];
+};
+__device__ __forceinline__ Raw16 raw8(const uint16_t *p) { return Raw16{*reinterpret_cast<const u32x4_any *>(p)}; }
+__device__ __forceinline__ Raw32 raw8(const float *p) {
+    Raw32 r;
+    r.w[0] = *reinterpret_cast<const u32x4_any *>(p);
+    r.w[1] = *reinterpret_cast<const u32x4_any *>(p + 4);
+    return r;
+}
+__device__ __forceinline__ F8 widen(const Raw16 &r) {
+    F8 f;
+    unpack8(r.w, f.v);
+    return f;
+}
+__device__ __forceinline__ F8 widen(const Raw32 &r) {
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f.v[i] = __uint_as_float(r.w[0][i]);
+        f.v[4 + i] = __uint_as_float(r.w[1][i]);
+    }
+    return f;
+}
+template <typename T>
+using RawOf = decltype(raw8((const T *)nullptr));
+
+// N groups of a row of n elements, group i at element at(i): all full groups are
+// requested before the first is used (a group that is not there asks for the
+// row's first), then the one that crosses the row's end is read element by
+// element.  `fill` past the end.
+template <typename T, int N>
+struct RowLoad {
+    RawOf<T> r[N];
+    template <typename At>
+    __device__ __forceinline__ void request(const T *row, int n, At at) {
+        if (n < 8) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = raw8(row + (at(i) + 8 <= n ? at(i) : 0));
+    }
+    template <typename At>
+    __device__ __forceinline__ F8 get(const T *row, int n, At at, int i, float fill = 0.0f) const {
+        const int c = at(i);
+        F8 f;
+        if (n >= 8) f = widen(r[i]);
+        if (c + 8 > n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] = c + e < n ? load1(row + c + e) : fill;
+        }
+        return f;
+    }
+};
+
 // The first cnt elements from p (any cnt; none for cnt <= 0), `fill` beyond.
 template <typename T>
 __device__ __forceinline__ F8 load8(const T *p, int64_t cnt, float fill = 0.0f) {
@@ -82,16 +139,32 @@ __device__ __forceinline__ void store8(T *p, int64_t cnt, const F8 &r) {
         if (i < cnt) store1(p + i, r.v[i]);
 }
 
-// Sum and maximum over the wave's 64 lanes, on every lane.
+// Sum and maximum over the wave's 64 lanes, on every lane: rows of 16 by shifted
+// adds, then the rows' totals passed on (DPP operands: no trip through LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or(float other, float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(other), __float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    v += dpp_or<0x111, 0xF>(0.0f, v);  // from 1, 2, 4, 8 lanes down the row
+    v += dpp_or<0x112, 0xF>(0.0f, v);
+    v += dpp_or<0x114, 0xF>(0.0f, v);
+    v += dpp_or<0x118, 0xF>(0.0f, v);
+    v += dpp_or<0x142, 0xA>(0.0f, v);  // lane 15 of rows 0 and 2 to rows 1 and 3
+    v += dpp_or<0x143, 0xC>(0.0f, v);  // lane 31 to rows 2 and 3
+    return last_lane(v);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    v = fmaxf(v, dpp_or<0x111, 0xF>(v, v));
+    v = fmaxf(v, dpp_or<0x112, 0xF>(v, v));
+    v = fmaxf(v, dpp_or<0x114, 0xF>(v, v));
+    v = fmaxf(v, dpp_or<0x118, 0xF>(v, v));
+    v = fmaxf(v, dpp_or<0x142, 0xA>(v, v));
+    v = fmaxf(v, dpp_or<0x143, 0xC>(v, v));
+    return last_lane(v);
 }
 
 }  // namespace qnf4

@@ -25,7 +25,7 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kMaxTensors = 48;        // 48 x 64 bytes of kernel arguments, of 4 KiB
+constexpr int kMaxTensors = 59;        // with the list's heads and the rates, 4 KiB of kernel arguments
 constexpr int kThreads = 256;
 constexpr int kChunk = kThreads * 8;   // elements a workgroup takes
 
@@ -35,6 +35,9 @@ struct TensorList {
     int count;
 };
 
+static_assert(sizeof(TensorList) + sizeof(AdamwHyper) <= 4096, "kernel arguments");
+
+constexpr float kFastEps = 1e-15f;  // beside it the root of a v below the normal numbers, 1e-19, is nothing
 constexpr float kMUnit = 1.0f / 16129.0f;       // 127^-2
 constexpr float kVUnit = 1.0f / 4228250625.0f;  // 255^-4, from 255^4 rounded to fp32
 
@@ -99,31 +102,68 @@ __device__ __forceinline__ float block_scale_of(float top, float unit) {
     return s >= 1.17549435e-38f ? s : 0.0f;
 }
 
-template <bool PF32, bool GF32, bool BITS8, bool MASTER>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(TensorList list, AdamwHyper h) {
+// rint of a root that the fast square root gives to 2 units in its last place:
+// exact unless the root lies so near to a half that these could matter; then
+// `near` is set, for the IEEE root to decide.
+__device__ __forceinline__ float root_code(float root, float band, bool &near) {
+    const float r = rintf(root);
+    near |= fabsf(fabsf(root - r) - 0.5f) < band;
+    return r;
+}
+
+// The step of 8 elements at `at`, cnt of them there.  FULL: all 8, with every
+// load requested before the first is used.
+template <bool PF32, bool GF32, bool BITS8, bool MASTER, bool FULL>
+__device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyper &h, int64_t at, int64_t cnt) {
     using P = std::conditional_t<PF32, float, uint16_t>;
     using G = std::conditional_t<GF32, float, uint16_t>;
-    const int k = tensor_of(list, blockIdx.x);
-    const AdamwTensor &t = list.t[k];
-    const int64_t at = (int64_t)(blockIdx.x - list.first[k]) * kChunk + threadIdx.x * 8;
-    const int64_t cnt = t.n - at;  // may be <= 0: such lanes hold zeros
     P *p = (P *)t.param + at;
     float *master = MASTER ? t.master + at : nullptr;
-    F8 g = load8((const G *)t.grad + at, cnt), m, v;
-    F8 w = MASTER ? load8((const float *)master, cnt) : load8((const P *)p, cnt);
+    F8 g, m, v, w;
     U8x8 mc, vc;
-    if (BITS8) {
-        mc = load_codes((const uint8_t *)t.m + at, cnt);
-        vc = load_codes((const uint8_t *)t.v + at, cnt);
-        const float ms = cnt > 0 ? t.m_scale[at >> 8] : 0.0f, vs = cnt > 0 ? t.v_scale[at >> 8] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m.v[i] = decode_m(mc, i, ms);
-            v.v[i] = decode_v(vc, i, vs);
+    float ms0 = 0.0f, vs0 = 0.0f;
+    if (FULL) {
+        const auto gr = raw8((const G *)t.grad + at);
+        RawOf<P> pr;
+        RawOf<float> wr, mr, vr;
+        if (MASTER) wr = raw8((const float *)master);
+        else pr = raw8((const P *)p);
+        if (BITS8) {
+            mc = load_codes((const uint8_t *)t.m + at, 8);
+            vc = load_codes((const uint8_t *)t.v + at, 8);
+            ms0 = t.m_scale[at >> 8];
+            vs0 = t.v_scale[at >> 8];
+        } else {
+            mr = raw8((const float *)t.m + at);
+            vr = raw8((const float *)t.v + at);
+        }
+        g = widen(gr);
+        w = MASTER ? widen(wr) : widen(pr);
+        if (!BITS8) {
+            m = widen(mr);
+            v = widen(vr);
         }
     } else {
-        m = load8((const float *)t.m + at, cnt);
-        v = load8((const float *)t.v + at, cnt);
+        g = load8((const G *)t.grad + at, cnt);
+        w = MASTER ? load8((const float *)master, cnt) : load8((const P *)p, cnt);
+        if (BITS8) {
+            mc = load_codes((const uint8_t *)t.m + at, cnt);
+            vc = load_codes((const uint8_t *)t.v + at, cnt);
+            if (cnt > 0) {
+                ms0 = t.m_scale[at >> 8];
+                vs0 = t.v_scale[at >> 8];
+            }
+        } else {
+            m = load8((const float *)t.m + at, cnt);
+            v = load8((const float *)t.v + at, cnt);
+        }
+    }
+    if (BITS8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m.v[i] = decode_m(mc, i, ms0);
+            v.v[i] = decode_v(vc, i, vs0);
+        }
     }
     float mtop = 0.0f, vtop = 0.0f;
 #pragma unroll
@@ -131,37 +171,71 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(TensorList list, AdamwH
         const float gi = g.v[i] * h.grad_scale;
         m.v[i] = m.v[i] * h.beta1 + gi * h.one_minus_beta1;
         v.v[i] = v.v[i] * h.beta2 + gi * gi * h.one_minus_beta2;
-        w.v[i] = w.v[i] * h.decay - h.step_size * (m.v[i] / (sqrtf(v.v[i]) * h.v_correction + h.eps));
         if (BITS8) {
             mtop = fmaxf(mtop, fabsf(m.v[i]));
             vtop = fmaxf(vtop, v.v[i]);
         }
     }
-    if (MASTER) store8(master, cnt, w);
-    store8(p, cnt, w);
+    if (h.eps >= kFastEps) {
+        // root and reciprocal to the last place each: the update's own error stays below 3 units of it
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = __builtin_amdgcn_sqrtf(v.v[i]) * h.v_correction + h.eps;
+            w.v[i] = w.v[i] * h.decay - h.step_size * (m.v[i] * __builtin_amdgcn_rcpf(d));
+        }
+    } else {  // a v below the normal numbers counts: these take it as 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w.v[i] = w.v[i] * h.decay - h.step_size * (m.v[i] / (sqrtf(v.v[i]) * h.v_correction + h.eps));
+    }
+    if (MASTER) store8(master, FULL ? 8 : cnt, w);
+    store8(p, FULL ? 8 : cnt, w);
     if (!BITS8) {
-        store8((float *)t.m + at, cnt, m);
-        store8((float *)t.v + at, cnt, v);
+        store8((float *)t.m + at, FULL ? 8 : cnt, m);
+        store8((float *)t.v + at, FULL ? 8 : cnt, v);
         return;
     }
     const float ms = block_scale_of(block_max(mtop), kMUnit), vs = block_scale_of(block_max(vtop), kVUnit);
     const float mi = ms > 0.0f ? 1.0f / ms : 0.0f, vi = vs > 0.0f ? 1.0f / vs : 0.0f;
+    float cm[8], cv[8];
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cm[i] = root_code(__builtin_amdgcn_sqrtf(fabsf(m.v[i]) * mi), 0x1p-15f, near);  // roots up to 127: 2 units are 2^-16
+        cv[i] = root_code(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v.v[i] * vi)), 0x1p-14f, near);  // up to 255
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cm[i] = rintf(sqrtf(fabsf(m.v[i]) * mi));
+            cv[i] = rintf(sqrtf(sqrtf(v.v[i] * vi)));
+        }
+    }
     mc.w[0] = mc.w[1] = vc.w[0] = vc.w[1] = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        int c = (int)fminf(rintf(sqrtf(fabsf(m.v[i]) * mi)), 127.0f);
+        int c = (int)fminf(cm[i], 127.0f);
         c = m.v[i] < 0.0f ? -c : c;
         mc.w[i >> 2] |= (uint32_t)(uint8_t)c << (8 * (i & 3));
-        int d = (int)fminf(rintf(sqrtf(sqrtf(v.v[i] * vi))), 255.0f);
+        int d = (int)fminf(cv[i], 255.0f);
         if (v.v[i] > 0.0f && vs > 0.0f && d < 1) d = 1;
         vc.w[i >> 2] |= (uint32_t)d << (8 * (i & 3));
     }
-    store_codes((uint8_t *)t.m + at, cnt, mc);
-    store_codes((uint8_t *)t.v + at, cnt, vc);
+    store_codes((uint8_t *)t.m + at, FULL ? 8 : cnt, mc);
+    store_codes((uint8_t *)t.v + at, FULL ? 8 : cnt, vc);
     if ((threadIdx.x & 31) == 0 && cnt > 0) {
         t.m_scale[at >> 8] = ms;
         t.v_scale[at >> 8] = vs;
     }
+}
+
+template <bool PF32, bool GF32, bool BITS8, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(TensorList list, AdamwHyper h) {
+    const int k = tensor_of(list, blockIdx.x);
+    const AdamwTensor &t = list.t[k];
+    const int64_t first = (int64_t)(blockIdx.x - list.first[k]) * kChunk, at = first + threadIdx.x * 8;
+    if (first + kChunk <= t.n) adamw_group<PF32, GF32, BITS8, MASTER, true>(t, h, at, 8);
+    else adamw_group<PF32, GF32, BITS8, MASTER, false>(t, h, at, t.n - at);  // a tensor's last workgroup
 }
 
 // The values that 8-bit states stand for; here param and grad are the fp32

@@ -73,10 +73,32 @@ __device__ __forceinline__ F8 widen(const Raw32 &r) {
 template <typename T>
 using RawOf = decltype(raw8((const T *)nullptr));
 
-// N groups of a row of n elements, group i at element at(i): all full groups are
-// requested before the first is used (a group that is not there asks for the
-// row's first), then the one that crosses the row's end is read element by
-// element.  `fill` past the end.
+// A group moved down by k elements, 0 <= k <= 8.
+__device__ __forceinline__ Raw16 moved(const Raw16 &r, int k) {
+    uint64_t lo = r.w[0] | (uint64_t)r.w[1] << 32, hi = r.w[2] | (uint64_t)r.w[3] << 32;
+    if (k & 4) {
+        lo = hi;
+        hi = 0;
+    }
+    const int s = 16 * (k & 3);
+    lo = lo >> s | (hi << 1) << (63 - s);
+    hi >>= s;
+    return Raw16{u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)}};
+}
+__device__ __forceinline__ Raw32 moved(Raw32 r, int k) {
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1) {
+        if (!(k & s)) continue;
+#pragma unroll
+        for (int i = 0; i + s < 8; ++i) r.w[i >> 2][i & 3] = r.w[(i + s) >> 2][(i + s) & 3];
+    }
+    return r;
+}
+
+// N groups of a row of n elements, group i at element at(i): all are requested
+// before the first is used, each whole and inside the row; the one that would
+// cross the row's end takes the row's last 8 elements and moves them down.
+// `fill` past the end.
 template <typename T, int N>
 struct RowLoad {
     RawOf<T> r[N];
@@ -84,16 +106,22 @@ struct RowLoad {
     __device__ __forceinline__ void request(const T *row, int n, At at) {
         if (n < 8) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = raw8(row + (at(i) + 8 <= n ? at(i) : 0));
+        for (int i = 0; i < N; ++i) r[i] = raw8(row + (at(i) + 8 <= n ? at(i) : n - 8));
     }
     template <typename At>
     __device__ __forceinline__ F8 get(const T *row, int n, At at, int i, float fill = 0.0f) const {
-        const int c = at(i);
+        const int c = at(i), left = n - c;
         F8 f;
-        if (n >= 8) f = widen(r[i]);
-        if (c + 8 > n) {
+        if (n < 8) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.v[e] = c + e < n ? load1(row + c + e) : fill;
+            for (int e = 0; e < 8; ++e) f.v[e] = e < left ? load1(row + c + e) : fill;
+            return f;
+        }
+        f = widen(r[i]);
+        if (__ballot(left < 8)) {  // only the wave that the row's end falls into
+            const F8 g = widen(moved(r[i], left > 0 && left < 8 ? 8 - left : 0));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] = e < left ? g.v[e] : fill;
         }
         return f;
     }

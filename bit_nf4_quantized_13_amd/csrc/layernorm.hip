@@ -15,10 +15,11 @@
 // 256 / TPR rows at a time.  Rows wider than kMaxHeld go through a kernel that
 // reads them again for each reduction (from L2).
 //
-// dw and db add over all rows: a workgroup of 1024 threads walks the rows with
-// its columns' sums in registers, adds its row groups' sums in LDS and writes
-// one partial row, and a second kernel adds the partial rows: fixed orders, so
-// the same bits on every run.
+// dw and db add over all rows: a workgroup of up to 1024 threads walks the rows
+// with its columns' sums in registers, adds its row groups' sums in LDS and
+// writes one partial row, and a second kernel adds the partial rows: fixed
+// orders, so the same bits on every run.  Above kMaxFused columns the sums find
+// no room beside the row, and a kernel of its own reads x and dy by columns.
 #include "elem8.hpp"
 #include "launch.hpp"
 
@@ -26,18 +27,19 @@ namespace qnf4 {
 namespace {
 
 constexpr int64_t kMaxHeld = 16384;    // widest row held in registers
+constexpr int64_t kMaxFused = 8192;    // and with its columns' sums beside it
 constexpr int kGradThreads = 1024;     // workgroup of the backward with parameter gradients
 constexpr int kMaxPartials = 256;      // its partial rows: one workgroup a CU
 constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
 
 // Sum of v over the TPR threads of a row group (TPR a multiple of 64); every
-// thread of the workgroup calls it.  red: one float for each wave.
+// thread of the workgroup calls it.  red: one float for each wave, not written
+// again before another barrier.
 template <int TPR>
 __device__ __forceinline__ float group_sum(float v, float *red) {
     v = wave_sum(v);
     if (TPR == 64) return v;
     const int wave = threadIdx.x >> 6, w0 = threadIdx.x / TPR * (TPR / 64);
-    __syncthreads();  // the last reading of red is done
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
     float s = 0.0f;
@@ -60,43 +62,51 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(
     const T *__restrict__ x, int64_t M, int64_t n, int64_t ldx, const W *__restrict__ w, const W *__restrict__ b,
     float eps, T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
     constexpr int kThreads = TPR > 256 ? TPR : 256;
-    __shared__ float red[kThreads / 64];
+    __shared__ float red[2][kThreads / 64];
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
     const bool live = row < M;
     const float inv_n = 1.0f / (float)n;
+    const int len = (int)n;
+    const T *xr = x + (live ? row : 0) * ldx;
+    auto at = [&](int i) { return (i * TPR + t) * 8; };
+    RowLoad<T, NV> xl;
+    RowLoad<W, NV> wl, bl;
+    xl.request(xr, len, at);
+    if (w) wl.request(w, len, at);
+    if (b) bl.request(b, len, at);
     F8 v[NV];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = ((int64_t)i * TPR + t) * 8;
-        v[i] = load8(x + row * ldx + c, live ? n - c : 0);
+        v[i] = xl.get(xr, len, at, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[i].v[e];
     }
-    const float mu = group_sum<TPR>(s, red) * inv_n;
+    const float mu = group_sum<TPR>(s, red[0]) * inv_n;
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = ((int64_t)i * TPR + t) * 8;
+        if (at(i) >= len) continue;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             v[i].v[e] -= mu;
-            if (c + e < n) q += v[i].v[e] * v[i].v[e];
+            if (at(i) + 8 <= len || at(i) + e < len) q += v[i].v[e] * v[i].v[e];
         }
     }
-    const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red) * inv_n + eps);
+    const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red[1]) * inv_n + eps);
     if (!live) return;
     if (t == 0 && mean) mean[row] = mu;
     if (t == 0 && rstd) rstd[row] = rs;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = ((int64_t)i * TPR + t) * 8;
-        if (c >= n) break;
-        const F8 wv = param8(w, c, n, 1.0f), bv = param8(b, c, n, 0.0f);
+        if (at(i) >= len) continue;
+        F8 wv, bv;
+        if (w) wv = wl.get(w, len, at, i);
+        if (b) bv = bl.get(b, len, at, i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i].v[e] = v[i].v[e] * rs * wv.v[e] + bv.v[e];
-        store8(y + row * n + c, n - c, v[i]);
+        for (int e = 0; e < 8; ++e) v[i].v[e] = v[i].v[e] * rs * (w ? wv.v[e] : 1.0f) + (b ? bv.v[e] : 0.0f);
+        store8(y + row * n + at(i), n - at(i), v[i]);
     }
 }
 
@@ -105,7 +115,7 @@ template <typename T, typename W>
 __global__ __launch_bounds__(kStreamThreads) void norm_fwd_stream_kernel(
     const T *__restrict__ x, int64_t n, int64_t ldx, const W *__restrict__ w, const W *__restrict__ b, float eps,
     T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
-    __shared__ float red[kStreamThreads / 64];
+    __shared__ float red[2][kStreamThreads / 64];
     const int64_t row = blockIdx.x;
     const T *xr = x + row * ldx;
     const float inv_n = 1.0f / (float)n;
@@ -115,14 +125,14 @@ __global__ __launch_bounds__(kStreamThreads) void norm_fwd_stream_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v.v[e];
     }
-    const float mu = group_sum<kStreamThreads>(s, red) * inv_n;
+    const float mu = group_sum<kStreamThreads>(s, red[0]) * inv_n;
     float q = 0.0f;
     for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
         const F8 v = load8(xr + c, n - c, mu);
 #pragma unroll
         for (int e = 0; e < 8; ++e) q += (v.v[e] - mu) * (v.v[e] - mu);
     }
-    const float rs = 1.0f / sqrtf(group_sum<kStreamThreads>(q, red) * inv_n + eps);
+    const float rs = 1.0f / sqrtf(group_sum<kStreamThreads>(q, red[1]) * inv_n + eps);
     if (threadIdx.x == 0 && mean) mean[row] = mu;
     if (threadIdx.x == 0 && rstd) rstd[row] = rs;
     for (int64_t c = threadIdx.x * 8; c < n; c += kStreamThreads * 8) {
@@ -142,10 +152,14 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     const T *__restrict__ x, const T *__restrict__ dy, int64_t M, int64_t n, int64_t ldx,
     const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx,
     float *__restrict__ part) {
-    constexpr int kGroups = THREADS / TPR;
-    __shared__ float red1[THREADS / 64], red2[THREADS / 64];
+    constexpr int kGroups = THREADS / TPR, kWavesRow = TPR / 64;
+    __shared__ float red[2][2][THREADS / 64];  // of the two sums, in turn from one pass over the rows to the next
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
+    const int len = (int)n;
     const float inv_n = 1.0f / (float)n;
+    auto at = [&](int i) { return (i * TPR + t) * 8; };
+    RowLoad<W, 1> wl;  // the weight stays in registers where there is one group a thread
+    if (w && NV == 1) wl.request(w, len, at);
     F8 dw[GRAD ? NV : 1], db[GRAD ? NV : 1];
     if (GRAD) {
 #pragma unroll
@@ -154,44 +168,72 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
             for (int e = 0; e < 8; ++e) dw[i].v[e] = db[i].v[e] = 0.0f;
     }
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < M; r0 += step) {
+    // the rows of the next pass are requested before this one's sums are waited for, where
+    // the registers hold both
+    constexpr bool kAhead = GRAD && NV == 1;
+    RowLoad<T, NV> xl, yl;
+    float mu, rs;
+    auto request = [&](int64_t row) {
+        const int64_t r = row < M ? row : 0;
+        xl.request(x + r * ldx, len, at);
+        yl.request(dy + r * n, len, at);
+        mu = mean[r];
+        rs = rstd[r];
+    };
+    if (kAhead) request((int64_t)blockIdx.x * kGroups + g);
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < M; r0 += step, turn ^= 1) {
         const int64_t row = r0 + g;
         const bool live = row < M;
-        const float mu = live ? mean[row] : 0.0f, rs = live ? rstd[row] : 0.0f;
+        if (!kAhead) request(row);
+        const T *xr = x + (live ? row : 0) * ldx, *yr = dy + (live ? row : 0) * n;
         F8 xh[NV], gr[NV];
         float s1 = 0.0f, s2 = 0.0f;
+        const float rs0 = rs;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = ((int64_t)i * TPR + t) * 8;
-            xh[i] = load8(x + row * ldx + c, live ? n - c : 0, mu);
-            gr[i] = load8(dy + row * n + c, live ? n - c : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = ((int64_t)i * TPR + t) * 8;
-            const F8 wv = param8(w, c, n, 1.0f);
+            xh[i] = xl.get(xr, len, at, i, mu);
+            gr[i] = yl.get(yr, len, at, i);
+            F8 wv;
+            if (w) wv = NV == 1 ? wl.get(w, len, at, 0) : param8(w, at(i), n, 1.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = (xh[i].v[e] - mu) * rs, d = gr[i].v[e];
+                const float h = (xh[i].v[e] - mu) * rs, d = live ? gr[i].v[e] : 0.0f;
                 if (GRAD) {
                     dw[i].v[e] += d * h;
                     db[i].v[e] += d;
                 }
                 xh[i].v[e] = h;
-                gr[i].v[e] = d * wv.v[e];
+                gr[i].v[e] = w ? d * wv.v[e] : d;
                 s1 += gr[i].v[e];
                 s2 += gr[i].v[e] * h;
             }
         }
-        const float c1 = group_sum<TPR>(s1, red1) * inv_n, c2 = group_sum<TPR>(s2, red2) * inv_n;
+        if (kAhead && r0 + step < M) request(row + step);
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if (TPR > 64) {
+            const int wave = threadIdx.x >> 6, w0 = g * kWavesRow;
+            if ((threadIdx.x & 63) == 0) {
+                red[turn][0][wave] = s1;
+                red[turn][1][wave] = s2;
+            }
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWavesRow; ++i) {
+                s1 += red[turn][0][w0 + i];
+                s2 += red[turn][1][w0 + i];
+            }
+        }
+        const float c1 = s1 * inv_n, c2 = s2 * inv_n;
         if (live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = ((int64_t)i * TPR + t) * 8;
                 F8 o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o.v[e] = rs * (gr[i].v[e] - c1 - xh[i].v[e] * c2);
-                if (c < n) store8(dx + row * n + c, n - c, o);
+                for (int e = 0; e < 8; ++e) o.v[e] = rs0 * (gr[i].v[e] - c1 - xh[i].v[e] * c2);
+                if (at(i) < len) store8(dx + row * n + at(i), n - at(i), o);
             }
         }
     }
@@ -305,14 +347,16 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restri
 }
 
 // The threads and groups of 8 a row of n takes, passed on as template values.
-template <typename F>
+template <bool FUSED, typename F>
 hipError_t held_shape(int64_t n, F f) {
     if (n <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-    if (n <= 1024) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    if (n <= 1024) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 1>());
     if (n <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (n <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-    if (n <= 8192) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+    if (n <= 4096) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 1>());
+    if (n <= 6144) return f(std::integral_constant<int, 768>(), std::integral_constant<int, 1>());
+    if (n <= kMaxFused) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 1>());
+    if constexpr (!FUSED) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+    return hipErrorInvalidValue;  // wider rows are not given to the fused kernel
 }
 
 template <typename T, typename W>
@@ -322,7 +366,7 @@ hipError_t norm_fwd(const T *x, int64_t M, int64_t n, int64_t ldx, const W *w, c
         norm_fwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, n, ldx, w, b, eps, y, mean, rstd);
         return hipGetLastError();
     }
-    return held_shape(n, [&](auto tpr, auto nv) {
+    return held_shape<false>(n, [&](auto tpr, auto nv) {
         constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
         norm_fwd_kernel<T, W, kTpr, decltype(nv)::value>
             <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, M, n, ldx, w, b, eps, y, mean, rstd);
@@ -333,36 +377,34 @@ hipError_t norm_fwd(const T *x, int64_t M, int64_t n, int64_t ldx, const W *w, c
 template <typename T, typename W>
 hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, const float *mean, const float *rstd,
                     const W *w, T *dx, float *dw, float *db, float *part, hipStream_t s) {
-    const bool grad = dw || db;
+    const bool grad = dw || db, fused = grad && n <= kMaxFused;
     int parts = 0;
     hipError_t e;
-    if (n > kMaxHeld) {
+    if (fused) {
+        e = held_shape<true>(n, [&](auto tpr, auto nv) {
+            constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 512 ? kTpr : kGradThreads, kRows = kThreads / kTpr;
+            const int64_t groups = (M + kRows - 1) / kRows;
+            parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
+            const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 32 KiB
+            norm_bwd_kernel<T, W, kThreads, kTpr, 1, true>
+                <<<parts, kThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part);
+            return hipGetLastError();
+        });
+    } else if (n <= kMaxHeld) {
+        e = held_shape<false>(n, [&](auto tpr, auto nv) {
+            constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
+            norm_bwd_kernel<T, W, kThreads, kTpr, decltype(nv)::value, false>
+                <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr);
+            return hipGetLastError();
+        });
+    } else {
         norm_bwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, dy, n, ldx, mean, rstd, w, dx);
         e = hipGetLastError();
-        if (!grad || e != hipSuccess) return e;
+    }
+    if (grad && !fused && e == hipSuccess) {
         parts = M < kMaxPartials ? (int)M : kMaxPartials;
         norm_cols_kernel<T><<<dim3((unsigned)((n + 2047) / 2048), parts), 256, 0, s>>>(x, dy, M, n, ldx, mean, rstd, part);
         e = hipGetLastError();
-    } else {
-        e = held_shape(n, [&](auto tpr, auto nv) {
-            constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
-            if (!grad) {
-                constexpr int kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
-                norm_bwd_kernel<T, W, kThreads, kTpr, kNv, false>
-                    <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr);
-                return hipGetLastError();
-            }
-            constexpr int kRows = kGradThreads / kTpr;
-            const int64_t groups = (M + kRows - 1) / kRows;
-            parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
-            const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 64 KiB
-            auto *kernel = norm_bwd_kernel<T, W, kGradThreads, kTpr, kNv, true>;
-            const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-            if (err != hipSuccess) return err;
-            kernel<<<parts, kGradThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part);
-            return hipGetLastError();
-        });
     }
     if (!grad || e != hipSuccess) return e;
     norm_reduce_kernel<<<(unsigned)((2 * n + 63) / 64), 1024, 0, s>>>(part, parts, n, dw, db);

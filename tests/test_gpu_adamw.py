@@ -155,6 +155,19 @@ def test_states_of_extreme_size():
     assert np.all(v[512:768] >= 1) and np.all(v[1280:] >= 1) and np.all(v[:256] == 0)
 
 
+def test_no_eps_and_gradients_below_the_normal_range_of_their_squares():
+    """eps = 0: the update is m over the root of v also where v is denormal."""
+    import bit_nf4_quantized_13_amd as q
+    say("adamw eps 0")
+    grad = torch.full((300,), 1e-20)
+    grad[::2] = -0.5
+    p = torch.zeros(300).cuda()
+    q.qlora_adamw_step(q.AdamWPlan.zeros([p], [grad.cuda()], bits8=False), lr=0.25, step=1, eps=0.0)
+    # v = 1e-3 g^2 (1e-43 for the small ones, held to 1 in 70 by its spacing), m = 0.1 g: the step is lr
+    assert np.all(np.abs(f32(p)[::2] - 0.25) <= 1e-6)
+    assert np.all(np.abs(f32(p)[1::2] + 0.25) <= 0.25 / 100)
+
+
 def test_8bit_states_follow_32bit_ones():
     """A quadratic's descent with 8-bit states ends where fp32 states end."""
     import bit_nf4_quantized_13_amd as q

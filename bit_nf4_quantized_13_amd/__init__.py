@@ -172,7 +172,9 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current device's current stream as a hipStream_t: torch.cuda.current_stream().cuda_stream
+    without the Stream object (0.1 against 2.9 us, which short calls notice)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev_tensor(t: torch.Tensor, dtype: torch.dtype, name: str) -> torch.Tensor:
@@ -608,7 +610,7 @@ def qlora_logprob_fwd(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
     kind, ld = _element_type(logits, "logits"), _rows(logits, "logits")
     m, v = logits.shape
     _shaped(targets, torch.int64, (m,), "targets")
-    logp, entropy, lse = (torch.empty(m, dtype=torch.float32, device=logits.device) for _ in range(3))
+    logp, entropy, lse = torch.empty((3, m), dtype=torch.float32, device=logits.device).unbind(0)
     top_logp = torch.empty((m, top), dtype=torch.float32, device=logits.device) if top > 0 else None
     top_ids = torch.empty((m, top), dtype=torch.int32, device=logits.device) if top > 0 else None
     ws = workspace if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), logits.device)

@@ -151,7 +151,7 @@ template <typename T, typename W, int THREADS, int TPR, int NV, bool GRAD>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     const T *__restrict__ x, const T *__restrict__ dy, int64_t M, int64_t n, int64_t ldx,
     const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx,
-    float *__restrict__ part) {
+    float *__restrict__ part, float *__restrict__ dweight, float *__restrict__ dbias) {
     constexpr int kGroups = THREADS / TPR, kWavesRow = TPR / 64;
     __shared__ float red[2][2][THREADS / 64];  // of the two sums, in turn from one pass over the rows to the next
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
@@ -240,7 +240,11 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     if (!GRAD) return;
     // the row groups' sums, added in group order
     extern __shared__ float sums[];  // [2][n], where there is more than one group
-    float *out = part + (int64_t)blockIdx.x * 2 * n;
+    float *out_w = part + (int64_t)blockIdx.x * 2 * n, *out_b = out_w + n;
+    if (gridDim.x == 1) {  // nothing to add to
+        out_w = dweight;
+        out_b = dbias;
+    }
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
         if (g == k) {
@@ -259,8 +263,8 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
                         sums[c + e] = a;
                         sums[n + c + e] = d;
                     } else {
-                        out[c + e] = a;
-                        out[n + c + e] = d;
+                        if (out_w) out_w[c + e] = a;
+                        if (out_b) out_b[c + e] = d;
                     }
                 }
             }
@@ -387,14 +391,15 @@ hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, 
             parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
             const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 32 KiB
             norm_bwd_kernel<T, W, kThreads, kTpr, 1, true>
-                <<<parts, kThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part);
+                <<<parts, kThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part, dw, db);
             return hipGetLastError();
         });
     } else if (n <= kMaxHeld) {
         e = held_shape<false>(n, [&](auto tpr, auto nv) {
             constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
             norm_bwd_kernel<T, W, kThreads, kTpr, decltype(nv)::value, false>
-                <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr);
+                <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr, nullptr,
+                                                                             nullptr);
             return hipGetLastError();
         });
     } else {
@@ -406,7 +411,7 @@ hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, 
         norm_cols_kernel<T><<<dim3((unsigned)((n + 2047) / 2048), parts), 256, 0, s>>>(x, dy, M, n, ldx, mean, rstd, part);
         e = hipGetLastError();
     }
-    if (!grad || e != hipSuccess) return e;
+    if (!grad || e != hipSuccess || (fused && parts == 1)) return e;
     norm_reduce_kernel<<<(unsigned)((2 * n + 63) / 64), 1024, 0, s>>>(part, parts, n, dw, db);
     return hipGetLastError();
 }

@@ -4,8 +4,9 @@
 //   the `top` largest x, equal ones in ascending order of index
 //   dx_v = g (delta_vt - p_v) - h p_v (log p_v + H)      g, h the gradients of logp and H
 // A logit of -inf is a forbidden token: p = 0, no part in H, gradient 0.  A row
-// of -inf only has lse = -inf, logp = -inf, H = 0 and gradient 0.  A target
-// outside [0, V) is no target: logp = 0 and g is not used.
+// of -inf only has lse = -inf, logp = -inf, H = 0 and gradient 0.  A NaN or +inf
+// makes its row's results NaN.  A target outside [0, V) is no target: logp = 0 and
+// g is not used.
 //
 // All sums in fp32.  H is taken from the deviations d, not as lse - sum p x:
 // that difference would lose digits in rows of large logits, and so would
@@ -76,6 +77,9 @@ __host__ __device__ inline Cut cut_of(int64_t V) {
     return Cut{(int)((V + len - 1) / len), len};
 }
 
+// A row of -inf only; a NaN, which no maximum shows, is in l.
+__device__ __forceinline__ bool none_left(float mx, float l) { return mx == -INFINITY && l == 0.0f; }
+
 // What a row's sums come to, written by one thread.
 struct RowOut {
     const int64_t *targets;
@@ -85,7 +89,7 @@ struct RowOut {
 template <typename T>
 __device__ __forceinline__ void write_row(const RowOut &o, int64_t row, const T *xr, int64_t V, float mx, float base,
                                           float l, float a) {
-    const bool none = mx == -INFINITY;
+    const bool none = none_left(mx, l);
     const float log_l = logf(l);
     if (o.lse) o.lse[row] = none ? -INFINITY : base + log_l;
     if (o.entropy) o.entropy[row] = none ? 0.0f : log_l - a / l;
@@ -196,13 +200,14 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     group_totals<THREADS>(l, a, red);
     if (large || a != a) {
         // ruled-out tokens (0 times -inf above): d held above the underflow of e^d, so that
-        // their part is 0; the same for the whole workgroup
+        // their part is 0, and a NaN kept; the same for the whole workgroup
         l = a = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = fmaxf((v[i].v[e] - base) * kLog2e, -200.0f);
+                float d = (v[i].v[e] - base) * kLog2e;
+                d = d < -200.0f ? -200.0f : d;
                 const float ex = __builtin_amdgcn_exp2f(d);
                 l += ex;
                 a = fmaf(ex, d, a);
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     const float log_l = logf(l);
     auto place = [&](int rank, u64 k) {
         if (ROW) {
-            out.top_logp[row * top + rank] = mx == -INFINITY ? -INFINITY : key_value(k) - base - log_l;
+            out.top_logp[row * top + rank] = none_left(mx, l) ? -INFINITY : key_value(k) - base - log_l;
             out.top_ids[row * top + rank] = (int32_t)key_index(k);
         } else {
             list[rank] = k;
@@ -284,8 +289,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
             __syncthreads();
         }
     }
-    if (!ROW)
-        for (int i = left + tid; i < top; i += THREADS) list[i] = 0;  // fewer elements than asked for
+    for (int i = n + tid; i < top; i += THREADS) place(i, 0);  // a chunk of fewer elements, or NaN
 }
 
 // One wave a row: the chunks' sums against the row's maximum, lane i holding
@@ -300,7 +304,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T *__restrict__ 
     const float *s = stats + (row * chunks + lane) * 4;
     const float m = mine ? s[0] : -INFINITY, mx = wave_max(m), base = mx == -INFINITY ? 0.0f : mx;
     float l = 0.0f, a = 0.0f;
-    if (mine && m > -INFINITY) {
+    if (mine && !none_left(m, s[1])) {
         const float d = fmaxf(m - base, -150.0f), f = expf(d);
         l = s[1] * f;
         a = (s[2] + s[1] * d) * f;
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T *__restrict__ 
             head = at < top ? list[at] : 0;
         }
         if (lane == 0) {
-            out.top_logp[row * top + i] = mx == -INFINITY ? -INFINITY : key_value(k) - base - log_l;
+            out.top_logp[row * top + i] = none_left(mx, l) ? -INFINITY : key_value(k) - base - log_l;
             out.top_ids[row * top + i] = (int32_t)key_index(k);
         }
     }
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void logprob_bwd_kernel(const T *x, int64
     const float base = none ? 0.0f : lse;
     const T *xr = x + row * ld;
     T *dr = dx + row * ldd;
-    float scale = 1.0f, log_s = 0.0f;  // p = scale e^(x - lse), log p = x - lse - log_s
+    float scale = base == base ? 1.0f : base, log_s = 0.0f;  // p = scale e^(x - lse), log p = x - lse - log_s
     if (fabsf(base) > kLargeLse) {     // the same for the whole workgroup
         __shared__ float red[kThreads / 64];
         float s = 0.0f;

@@ -169,6 +169,32 @@ def test_large_and_close_logits():
     check(x, torch.tensor([1, 2, 17]).cuda(), 3, 1)
 
 
+def test_a_row_with_nan_or_infinity():
+    """Its results are NaN, its gradient too; the other rows keep their bits and the indices stay in range."""
+    import bit_nf4_quantized_13_amd as q
+    for v, rows in ((40, 6), (9000, 6), (9000, 300), (40000, 6)):
+        say(f"logprob NaN V={v} rows={rows}")
+        x = logits(rows, v, torch.bfloat16, v)
+        t = torch.arange(rows).cuda() % 7
+        clean = q.qlora_logprob_fwd(x, t, top=5)
+        dl, de = torch.ones(rows, device="cuda"), torch.ones(rows, device="cuda")
+        want = q.qlora_logprob_bwd(x, t, clean[2], clean[1], dl, de)
+        x[1, v - 2] = float("nan")
+        x[2, :] = float("nan")
+        x[3, 17] = INF
+        x[4, :] = -INF
+        x[4, 3] = float("nan")
+        logp, ent, lse, tl, ti = q.qlora_logprob_fwd(x, t, top=5)
+        d = q.qlora_logprob_bwd(x, t, lse, None, dl, None)
+        d2 = q.qlora_logprob_bwd(x, t, lse, ent, dl, de)
+        bad, keep = [1, 2, 3, 4], [0, *range(5, rows)]
+        for r in (logp, ent, lse, tl, d, d2):
+            assert bool(r[bad].isnan().all())
+        assert bool(((ti >= -1) & (ti < v)).all())
+        for a, b in zip((logp, ent, lse, tl, ti, d2), (*clean, want)):
+            assert torch.equal(a[keep], b[keep])
+
+
 def test_in_place_gradient_and_reruns():
     import bit_nf4_quantized_13_amd as q
     say("logprob in place")

@@ -658,11 +658,18 @@ __global__ __launch_bounds__(kThreads) void attention_group_sum_kernel(Attention
 
 int slots_of(const AttentionShape &a) { return a.T / kOwn + a.S + 2; }
 
-// A workgroup a head instead of a group in the dk, dv kernel: where the groups'
-// tiles would give each CU less than two rounds of its two workgroups, and the
-// longest of them, the first keys of a sequence with all heads' rows, would run
-// alone at the end.
-bool split_heads(const AttentionShape &a) { return a.H > a.Hk && (int64_t)(a.T / kOwn) * a.Hk < 1024; }
+// A workgroup a head instead of a group in the dk, dv kernel.  With a group a
+// workgroup, the first keys of a sequence of L rows take group L / 32 steps, and the
+// launch no less; shared evenly over the 512 resident workgroups, all of them would
+// take T H L / 2^22.  The partials cost 16 T H D bytes of traffic, as much as about
+// T H / 2700 steps, and half of the uneven rest is won back (workgroups alone on a
+// CU run faster).  L is the mean length T / S: the lengths are on the device.  Backward
+// in all (us, a head / a group a workgroup), D = 128, H / Hk = 32 / 8: 4 x 1024 228 / 266, 4 x 2048 590 / 640,
+// 1 x 8192 1805 / 2315; 8 x 1024 408 / 353, 16 x 512 329 / 238, 16 x 1024 783 / 674.
+bool split_heads(const AttentionShape &a) {
+    const double len = a.T / a.S;
+    return a.H > a.Hk && len * 131072 > (double)a.T * a.Hk * (len + 1536);
+}
 size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
 
 template <int DP>

@@ -10,26 +10,35 @@
 // larger than its spread keeps its variance; one rounding at the store.
 //
 // Bound: HBM (8 to 14 flops an element).  x (and dy) are read once and held in
-// registers over the reductions: a row is spread over TPR threads of 8 NV
-// elements each, TPR and NV the smallest that hold n; 256 threads take
-// 256 / TPR rows at a time.  Rows wider than kMaxHeld go through a kernel that
-// reads them again for each reduction (from L2).
+// registers over the reductions: a row is spread over TPR threads of 8 elements
+// each, TPR the smallest that holds n; 256 threads take 256 / TPR rows at a time.
+// Rows wider than kMaxHeld go through a kernel that reads them again for each
+// reduction, from L2 (a thread with 16 elements held is slower: 4096 x 12288
+// forward 62 us against 44, backward 72 against 69).
 //
 // dw and db add over all rows: a workgroup of up to 1024 threads walks the rows
 // with its columns' sums in registers, adds its row groups' sums in LDS and
 // writes one partial row, and a second kernel adds the partial rows: fixed
-// orders, so the same bits on every run.  Above kMaxFused columns the sums find
-// no room beside the row, and a kernel of its own reads x and dy by columns.
+// orders, so the same bits on every run.  For rows wider than kMaxHeld a kernel
+// of its own reads x and dy by columns (4096 x 6144: 43 us in one pass, 64 in two).
+//
+// Measured: 4096 x 8192 bf16 with dw and db 36.4 + 4.9 us for 201 MB (5.5 TB/s in
+// the main kernel; a copy reaches 5.2); 1531 x 2753 fp32 dx alone 11.2 us for 51 MB; one row
+// of 4096 forward 2.2 us.
 #include "elem8.hpp"
 #include "launch.hpp"
 
 namespace qnf4 {
 namespace {
 
-constexpr int64_t kMaxHeld = 16384;    // widest row held in registers
-constexpr int64_t kMaxFused = 8192;    // and with its columns' sums beside it
+constexpr int64_t kMaxHeld = 8192;     // widest row held in registers
 constexpr int kGradThreads = 1024;     // workgroup of the backward with parameter gradients
-constexpr int kMaxPartials = 256;      // its partial rows: one workgroup a CU
+constexpr int kMaxPartials = 256;      // its partial rows: one workgroup a CU (128: 8192 x 4096 58 us against 43)
+// The backward without them: workgroups that walk over rows as well, the next row's loads
+// under way (8192 x 4096 bf16: 34 us; a workgroup a row 45), two a CU.  The forward, with one load
+// less to wait for, is as fast or faster with a workgroup a row (4096 x 8192: 29 us against 35).
+constexpr int kRowThreads = 512;
+constexpr int kMaxRowGroups = 512;
 constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
 
 // Sum of v over the TPR threads of a row group (TPR a multiple of 64); every
@@ -57,7 +66,7 @@ __device__ __forceinline__ F8 param8(const T *p, int64_t c, int64_t n, float fil
     return r;
 }
 
-template <typename T, typename W, int TPR, int NV>
+template <typename T, typename W, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(
     const T *__restrict__ x, int64_t M, int64_t n, int64_t ldx, const W *__restrict__ w, const W *__restrict__ b,
     float eps, T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
@@ -67,47 +76,38 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(
     const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
     const bool live = row < M;
     const float inv_n = 1.0f / (float)n;
-    const int len = (int)n;
+    const int len = (int)n, c = t * 8;
     const T *xr = x + (live ? row : 0) * ldx;
-    auto at = [&](int i) { return (i * TPR + t) * 8; };
-    RowLoad<T, NV> xl;
-    RowLoad<W, NV> wl, bl;
+    auto at = [&](int) { return c; };
+    RowLoad<T, 1> xl;
+    RowLoad<W, 1> wl, bl;
     xl.request(xr, len, at);
     if (w) wl.request(w, len, at);
     if (b) bl.request(b, len, at);
-    F8 v[NV];
+    F8 v = xl.get(xr, len, at, 0);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        v[i] = xl.get(xr, len, at, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[i].v[e];
-    }
+    for (int e = 0; e < 8; ++e) s += v.v[e];
     const float mu = group_sum<TPR>(s, red[0]) * inv_n;
     float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (at(i) >= len) continue;
+    if (c < len) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[i].v[e] -= mu;
-            if (at(i) + 8 <= len || at(i) + e < len) q += v[i].v[e] * v[i].v[e];
+            v.v[e] -= mu;
+            if (c + 8 <= len || c + e < len) q += v.v[e] * v.v[e];
         }
     }
     const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red[1]) * inv_n + eps);
     if (!live) return;
     if (t == 0 && mean) mean[row] = mu;
     if (t == 0 && rstd) rstd[row] = rs;
+    if (c >= len) return;
+    F8 wv, bv;
+    if (w) wv = wl.get(w, len, at, 0);
+    if (b) bv = bl.get(b, len, at, 0);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (at(i) >= len) continue;
-        F8 wv, bv;
-        if (w) wv = wl.get(w, len, at, i);
-        if (b) bv = bl.get(b, len, at, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i].v[e] = v[i].v[e] * rs * (w ? wv.v[e] : 1.0f) + (b ? bv.v[e] : 0.0f);
-        store8(y + row * n + at(i), n - at(i), v[i]);
-    }
+    for (int e = 0; e < 8; ++e) v.v[e] = v.v[e] * rs * (w ? wv.v[e] : 1.0f) + (b ? bv.v[e] : 0.0f);
+    store8(y + row * n + c, n - c, v);
 }
 
 // Rows wider than the registers hold: one workgroup a row, read three times.
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kStreamThreads) void norm_fwd_stream_kernel(
 // dX, and with GRAD the workgroup's partial row of dw and db ([2][n] at
 // part + blockIdx.x 2 n).  Row group g of the workgroup takes the rows
 // blockIdx.x GROUPS + g, then every gridDim.x GROUPS-th.
-template <typename T, typename W, int THREADS, int TPR, int NV, bool GRAD>
+template <typename T, typename W, int THREADS, int TPR, bool GRAD>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     const T *__restrict__ x, const T *__restrict__ dy, int64_t M, int64_t n, int64_t ldx,
     const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx,
@@ -155,23 +155,16 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     constexpr int kGroups = THREADS / TPR, kWavesRow = TPR / 64;
     __shared__ float red[2][2][THREADS / 64];  // of the two sums, in turn from one pass over the rows to the next
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
-    const int len = (int)n;
+    const int len = (int)n, c = t * 8;
     const float inv_n = 1.0f / (float)n;
-    auto at = [&](int i) { return (i * TPR + t) * 8; };
-    RowLoad<W, 1> wl;  // the weight stays in registers where there is one group a thread
-    if (w && NV == 1) wl.request(w, len, at);
-    F8 dw[GRAD ? NV : 1], db[GRAD ? NV : 1];
-    if (GRAD) {
+    auto at = [&](int) { return c; };
+    RowLoad<W, 1> wl;  // the weight stays in registers
+    if (w) wl.request(w, len, at);
+    F8 dw, db;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dw[i].v[e] = db[i].v[e] = 0.0f;
-    }
+    for (int e = 0; e < 8; ++e) dw.v[e] = db.v[e] = 0.0f;
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    // the rows of the next pass are requested before this one's sums are waited for, where
-    // the registers hold both
-    constexpr bool kAhead = GRAD && NV == 1;
-    RowLoad<T, NV> xl, yl;
+    RowLoad<T, 1> xl, yl;
     float mu, rs;
     auto request = [&](int64_t row) {
         const int64_t r = row < M ? row : 0;
@@ -180,36 +173,29 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
         mu = mean[r];
         rs = rstd[r];
     };
-    if (kAhead) request((int64_t)blockIdx.x * kGroups + g);
+    request((int64_t)blockIdx.x * kGroups + g);
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < M; r0 += step, turn ^= 1) {
         const int64_t row = r0 + g;
         const bool live = row < M;
-        if (!kAhead) request(row);
-        const T *xr = x + (live ? row : 0) * ldx, *yr = dy + (live ? row : 0) * n;
-        F8 xh[NV], gr[NV];
         float s1 = 0.0f, s2 = 0.0f;
         const float rs0 = rs;
+        F8 xh = xl.get(x + (live ? row : 0) * ldx, len, at, 0, mu), gr = yl.get(dy + (live ? row : 0) * n, len, at, 0), wv;
+        if (w) wv = wl.get(w, len, at, 0);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            xh[i] = xl.get(xr, len, at, i, mu);
-            gr[i] = yl.get(yr, len, at, i);
-            F8 wv;
-            if (w) wv = NV == 1 ? wl.get(w, len, at, 0) : param8(w, at(i), n, 1.0f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float h = (xh[i].v[e] - mu) * rs, d = live ? gr[i].v[e] : 0.0f;
-                if (GRAD) {
-                    dw[i].v[e] += d * h;
-                    db[i].v[e] += d;
-                }
-                xh[i].v[e] = h;
-                gr[i].v[e] = w ? d * wv.v[e] : d;
-                s1 += gr[i].v[e];
-                s2 += gr[i].v[e] * h;
+        for (int e = 0; e < 8; ++e) {
+            const float h = (xh.v[e] - mu) * rs, d = live ? gr.v[e] : 0.0f;
+            if (GRAD) {
+                dw.v[e] += d * h;
+                db.v[e] += d;
             }
+            xh.v[e] = h;
+            gr.v[e] = w ? d * wv.v[e] : d;
+            s1 += gr.v[e];
+            s2 += gr.v[e] * h;
         }
-        if (kAhead && r0 + step < M) request(row + step);
+        // the rows of the next pass are requested before this one's sums are waited for
+        if (r0 + step < M) request(row + step);
         s1 = wave_sum(s1);
         s2 = wave_sum(s2);
         if (TPR > 64) {
@@ -227,14 +213,11 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
             }
         }
         const float c1 = s1 * inv_n, c2 = s2 * inv_n;
-        if (live) {
+        if (live && c < len) {
+            F8 o;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                F8 o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o.v[e] = rs0 * (gr[i].v[e] - c1 - xh[i].v[e] * c2);
-                if (at(i) < len) store8(dx + row * n + at(i), n - at(i), o);
-            }
+            for (int e = 0; e < 8; ++e) o.v[e] = rs0 * (gr.v[e] - c1 - xh.v[e] * c2);
+            store8(dx + row * n + c, n - c, o);
         }
     }
     if (!GRAD) return;
@@ -247,26 +230,21 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
     }
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        if (g == k) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = ((int64_t)i * TPR + t) * 8;
+        if (g == k && c < len) {
+            if (k > 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (c + e >= n) continue;
-                    float a = dw[GRAD ? i : 0].v[e], d = db[GRAD ? i : 0].v[e];
-                    if (k > 0) {
-                        a += sums[c + e];
-                        d += sums[n + c + e];
-                    }
-                    if (k + 1 < kGroups) {
-                        sums[c + e] = a;
-                        sums[n + c + e] = d;
-                    } else {
-                        if (out_w) out_w[c + e] = a;
-                        if (out_b) out_b[c + e] = d;
-                    }
+                    if (c + e >= len) continue;
+                    dw.v[e] += sums[c + e];
+                    db.v[e] += sums[len + c + e];
                 }
+            }
+            if (k + 1 < kGroups) {
+                store8(sums + c, n - c, dw);
+                store8(sums + len + c, n - c, db);
+            } else {
+                if (out_w) store8(out_w + c, n - c, dw);
+                if (out_b) store8(out_b + c, n - c, db);
             }
         }
         if (k + 1 < kGroups) __syncthreads();
@@ -335,8 +313,14 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restri
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
-    if (c < 2 * n)
-        for (int p = wave; p < parts; p += 16) s += part[(int64_t)p * 2 * n + c];
+    if (c < 2 * n) {
+        // kMaxPartials / 16 loads at once
+        float v[kMaxPartials / 16];
+#pragma unroll
+        for (int i = 0; i < kMaxPartials / 16; ++i) v[i] = wave + 16 * i < parts ? part[(int64_t)(wave + 16 * i) * 2 * n + c] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxPartials / 16; ++i) s += v[i];
+    }
     sums[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= 2 * n) return;
@@ -350,17 +334,15 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restri
     }
 }
 
-// The threads and groups of 8 a row of n takes, passed on as template values.
-template <bool FUSED, typename F>
+// The threads a row of n takes, passed on as a template value.
+template <typename F>
 hipError_t held_shape(int64_t n, F f) {
-    if (n <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-    if (n <= 1024) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 1>());
-    if (n <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (n <= 4096) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 1>());
-    if (n <= 6144) return f(std::integral_constant<int, 768>(), std::integral_constant<int, 1>());
-    if (n <= kMaxFused) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 1>());
-    if constexpr (!FUSED) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
-    return hipErrorInvalidValue;  // wider rows are not given to the fused kernel
+    if (n <= 512) return f(std::integral_constant<int, 64>());
+    if (n <= 1024) return f(std::integral_constant<int, 128>());
+    if (n <= 2048) return f(std::integral_constant<int, 256>());
+    if (n <= 4096) return f(std::integral_constant<int, 512>());
+    if (n <= 6144) return f(std::integral_constant<int, 768>());
+    return f(std::integral_constant<int, 1024>());
 }
 
 template <typename T, typename W>
@@ -370,9 +352,9 @@ hipError_t norm_fwd(const T *x, int64_t M, int64_t n, int64_t ldx, const W *w, c
         norm_fwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, n, ldx, w, b, eps, y, mean, rstd);
         return hipGetLastError();
     }
-    return held_shape<false>(n, [&](auto tpr, auto nv) {
+    return held_shape(n, [&](auto tpr) {
         constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
-        norm_fwd_kernel<T, W, kTpr, decltype(nv)::value>
+        norm_fwd_kernel<T, W, kTpr>
             <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, M, n, ldx, w, b, eps, y, mean, rstd);
         return hipGetLastError();
     });
@@ -381,25 +363,25 @@ hipError_t norm_fwd(const T *x, int64_t M, int64_t n, int64_t ldx, const W *w, c
 template <typename T, typename W>
 hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, const float *mean, const float *rstd,
                     const W *w, T *dx, float *dw, float *db, float *part, hipStream_t s) {
-    const bool grad = dw || db, fused = grad && n <= kMaxFused;
+    const bool grad = dw || db, fused = grad && n <= kMaxHeld;
     int parts = 0;
     hipError_t e;
     if (fused) {
-        e = held_shape<true>(n, [&](auto tpr, auto nv) {
+        e = held_shape(n, [&](auto tpr) {
             constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 512 ? kTpr : kGradThreads, kRows = kThreads / kTpr;
             const int64_t groups = (M + kRows - 1) / kRows;
             parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
             const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 32 KiB
-            norm_bwd_kernel<T, W, kThreads, kTpr, 1, true>
+            norm_bwd_kernel<T, W, kThreads, kTpr, true>
                 <<<parts, kThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part, dw, db);
             return hipGetLastError();
         });
     } else if (n <= kMaxHeld) {
-        e = held_shape<false>(n, [&](auto tpr, auto nv) {
-            constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 256 ? kTpr : 256, kRows = kThreads / kTpr;
-            norm_bwd_kernel<T, W, kThreads, kTpr, decltype(nv)::value, false>
-                <<<(unsigned)((M + kRows - 1) / kRows), kThreads, 0, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, nullptr, nullptr,
-                                                                             nullptr);
+        e = held_shape(n, [&](auto tpr) {
+            constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > kRowThreads ? kTpr : kRowThreads, kRows = kThreads / kTpr;
+            const int64_t groups = (M + kRows - 1) / kRows;
+            norm_bwd_kernel<T, W, kThreads, kTpr, false><<<(unsigned)(groups < kMaxRowGroups ? groups : kMaxRowGroups), kThreads, 0, s>>>(
+                x, dy, M, n, ldx, mean, rstd, w, dx, nullptr, nullptr, nullptr);
             return hipGetLastError();
         });
     } else {

@@ -25,13 +25,13 @@
 //   dq       S' = K Q', dP' = V dO', dQ' += K' dS'
 //   dk, dv   S = Q K',  dP = dO V',  dV' += dO' P, dK' += Q' dS
 // Scores, statistics, sums and gradients are fp32; P and dS are rounded to bf16
-// for their product, which the matrix cores take no wider (relative 2^-9, as
+// for their product, which the matrix cores take no wider (relative 2^-8, as
 // every stored input).  Backward, the score products start from -lse / scale and
 // the dp products from -delta, so that their results are the exponent and the
 // second factor of ds at once.  delta's o is taken with its rounding residual where the
 // forward saved it, so that the bf16 of o does not enter dS.
 //
-// A workgroup is 4 waves with 32 rows each; the 64-row tiles of the other side
+// A workgroup is 4 waves (or two parts of 4) with 32 rows each; the tiles of the other side
 // are brought to LDS by direct transfers, one tile ahead.  Tile rows are 16-byte
 // chunks in an order that depends on the row, so that both the row reads (one
 // chunk of 16 rows) and the transposing reads (4 chunks of 4 rows) fall on all
@@ -45,7 +45,7 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;          // of a workgroup with one part
 constexpr int kThreads = 64 * kWaves;
 constexpr int kOwn = 32 * kWaves;  // rows a workgroup owns
 constexpr int kStream = 64;        // rows of a tile that passes through LDS
@@ -152,9 +152,9 @@ __device__ __forceinline__ void transfer4(__amdgpu_buffer_rsrc_t r, uint32_t dst
 // the row group's number.  KEEP: the offsets stay in registers over the kernel;
 // otherwise two registers hold them and they are formed at every tile, for a
 // kernel that has no registers left.
-template <int DP, int ROWS, bool KEEP>
+template <int DP, int ROWS, int WAVES, bool KEEP>
 struct Mover {
-    static constexpr int kChunks = DP / 8, kRows = 64 / kChunks, kOwnRows = ROWS / kWaves, kOps = kOwnRows / kRows;
+    static constexpr int kChunks = DP / 8, kRows = 64 / kChunks, kOwnRows = ROWS / WAVES, kOps = kOwnRows / kRows;
     uint32_t base, chunk, off[KEEP ? kOps : 1];
     __device__ __forceinline__ uint32_t offset(uint32_t base, uint32_t chunk, int64_t ld, int D, int i) const {
         const uint32_t c = chunk ^ swizzle<DP>(i * kRows);
@@ -195,11 +195,12 @@ template <int DP, bool KEEP>
 struct Reader {
     static constexpr int kSteps = DP / 16, kTiles = DP / 32, kRow = DP * 2;
     uint32_t row0, col0, row[KEEP ? kSteps : 1], col[KEEP ? kSteps : 1];
-    __device__ __forceinline__ void init() {
+    // first: of the tile's rows, a multiple of 32
+    __device__ __forceinline__ void init(int first) {
         const int l = threadIdx.x & 63, h = l >> 5, r = l & 31, i = l & 15, g = (l >> 4) & 1;
-        row0 = r * kRow + (h ^ swizzle<DP>(r)) * 16;
+        row0 = (first + r) * kRow + (h ^ swizzle<DP>(r)) * 16;
         const int rr = 4 * h + i / 4;
-        col0 = rr * kRow + ((g * 2 + (i & 3) / 2) ^ swizzle<DP>(rr)) * 16 + (i & 1) * 8;
+        col0 = (first + rr) * kRow + ((g * 2 + (i & 3) / 2) ^ swizzle<DP>(rr)) * 16 + (i & 1) * 8;
         if (KEEP) {
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
@@ -261,7 +262,7 @@ __device__ __forceinline__ void store_rows(uint16_t *y, uint16_t *res, int64_t l
 // Zeros in the rows [row0, end) of one head, by the whole workgroup.
 __device__ __forceinline__ void zero_rows(uint16_t *y, int64_t ld, int row0, int end, int D) {
     const int chunks = D / 8;
-    for (int i = threadIdx.x; i < kOwn * chunks; i += kThreads) {
+    for (int i = threadIdx.x; i < kOwn * chunks; i += blockDim.x) {
         const int row = row0 + i / chunks;
         if (row < end) *reinterpret_cast<uint4 *>(y + (int64_t)row * ld + (i % chunks) * 8) = make_uint4(0, 0, 0, 0);
     }
@@ -271,14 +272,35 @@ __device__ __forceinline__ void zero_rows(uint16_t *y, int64_t ld, int row0, int
 // heads, so that the heads of a group and the tiles of a head meet in one L2.
 __device__ __forceinline__ int head_of(int p, int H, int Hk) { return (p % Hk) * (H / Hk) + p / Hk; }
 
-template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
+// Where there are few workgroups, PARTS = 2 groups of 4 waves share a workgroup's rows,
+// each with its own rows of every tile, and their results meet in LDS at the end: a
+// lane's registers, 64 apart.
+template <int N>
+__device__ __forceinline__ void put_tiles(float *to, const f32x16 *t) {
+#pragma unroll
+    for (int dt = 0; dt < N; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) to[(dt * 16 + i) * 64] = t[dt][i];
+}
+template <int N>
+__device__ __forceinline__ void add_tiles(f32x16 *t, float f, const float *from, float g) {
+#pragma unroll
+    for (int dt = 0; dt < N; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[dt][i] = t[dt][i] * f + from[(dt * 16 + i) * 64] * g;
+}
+
+template <int DP, int PARTS>
+__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
                                                                  const uint16_t *__restrict__ k,
                                                                  const uint16_t *__restrict__ v,
                                                                  const int32_t *__restrict__ cu,
                                                                  uint16_t *__restrict__ o, uint16_t *__restrict__ res,
                                                                  float *__restrict__ lse, int slots) {
-    __shared__ __attribute__((aligned(256))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
+    constexpr int kStep = kStream * PARTS;
+    __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStep * DP];
+    uint16_t(*ks_)[kStep * DP] = tiles_, (*vs_)[kStep * DP] = tiles_ + 2;
+    __shared__ float meet[2][PARTS > 1 ? kThreads : 1];
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     // the long rows' tiles first
     const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
@@ -288,16 +310,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionSha
     if (at.outside) {
         zero_rows(o + head * a.D, ldo, at.first, last, a.D);
         if (res) zero_rows(res + head * a.D, ldo, at.first, last, a.D);
-        for (int i = at.first + threadIdx.x; i < last; i += kThreads) lse[(int64_t)head * a.T + i] = -INFINITY;
+        for (int i = at.first + threadIdx.x; i < last; i += kThreads * PARTS) lse[(int64_t)head * a.T + i] = -INFINITY;
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
     const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP, kStream, true> mk, mv;
+    Mover<DP, kStep, kWaves * PARTS, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
     Reader<DP, true> rd;
-    rd.init();
+    rd.init(kStream * part);
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     bf16x8 qf[DP / 16];
     load_rows<DP>(q + (int64_t)head * a.D, a.ldq, row0, at.end, a.D, qf);
@@ -308,17 +331,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionSha
         for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
     float m = -INFINITY, sum = 0.0f;
     const float c = a.scale * kLog2e;
-    const int tiles = (last - at.begin + kStream - 1) / kStream;
+    const int tiles = (last - at.begin + kStep - 1) / kStep;
     mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
     mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
     // B: the buffer that tile j is in, a constant so that it is part of the instructions' offsets
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
         __syncthreads();  // tile j is in LDS, and nobody reads the other buffer
-        const int key0 = at.begin + j * kStream;
+        const int tile0 = at.begin + j * kStep, key0 = tile0 + kStream * part;
         if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, a.D, key0 + kStream, at.end, lds_addr(ks_[1 - B]));
-            mv.load(vh, a.ldv, a.D, key0 + kStream, at.end, lds_addr(vs_[1 - B]));
+            mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
+            mv.load(vh, a.ldv, a.D, tile0 + kStep, at.end, lds_addr(vs_[1 - B]));
         }
         if (key0 > row0 + 31) return;  // the wave's rows all come before this tile
         const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
@@ -348,14 +371,15 @@ __global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionSha
         if (__ballot((top - m) * c > 8.0f)) {
             const float old = m;
             m = fmaxf(m, top);
-            const float f = __builtin_amdgcn_exp2f((old - m) * c);
+            // a second part may not have met a key that the row attends to
+            const float f = PARTS > 1 && m == old ? 1.0f : __builtin_amdgcn_exp2f((old - m) * c);
             sum *= f;
 #pragma unroll
             for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
         }
-        const float mc = m * c;
+        const float mc = PARTS > 1 && m == -INFINITY ? 0.0f : m * c;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -375,18 +399,35 @@ __global__ __launch_bounds__(kThreads, 2) void attention_fwd_kernel(AttentionSha
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     sum = pair_sum(sum);
+    if (PARTS > 1) {
+        float *other = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64 + l;
+        __syncthreads();  // the tiles are read
+        if (part == 1) {
+            put_tiles<DP / 32>(other, acc);
+            meet[0][wave * 64 + l] = m;
+            meet[1][wave * 64 + l] = sum;
+        }
+        __syncthreads();
+        if (part == 1) return;
+        const float m1 = meet[0][wave * 64 + l], top = fmaxf(m, m1);
+        const float f0 = __builtin_amdgcn_exp2f((m - top) * c), f1 = __builtin_amdgcn_exp2f((m1 - top) * c);
+        add_tiles<DP / 32>(acc, f0, other, f1);
+        sum = sum * f0 + meet[1][wave * 64 + l] * f1;
+        m = top;
+    }
     store_rows<DP>(o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
     if (h == 0 && row < at.end) lse[(int64_t)head * a.T + row] = m * a.scale + logf(sum);
 }
 
 // dq, and the rows' statistics for the dk, dv kernel.
-template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
+template <int DP, int PARTS>
+__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
     const uint16_t *__restrict__ o, const uint16_t *__restrict__ res, const float *__restrict__ lse,
     const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, uint16_t *__restrict__ dq, int64_t lddq,
     float *__restrict__ stats, int slots) {
-    __shared__ __attribute__((aligned(256))) uint16_t ks_[2][kStream * DP], vs_[2][kStream * DP];
+    __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStream * DP];
+    uint16_t(*ks_)[kStream * DP] = tiles_, (*vs_)[kStream * DP] = tiles_ + 2;
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
@@ -396,13 +437,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
         zero_rows(dq + head * a.D, lddq, at.first, last, a.D);
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
     const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP, kStream, true> mk, mv;
+    Mover<DP, kStream, kWaves * PARTS, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
     Reader<DP, true> rd;
-    rd.init();
+    rd.init(32 * part);
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     const int tiles = (last - at.begin + kStream - 1) / kStream;
     mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
@@ -429,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
     dl = pair_sum(dl);
     dl = -dl;
     const float ls = row < at.end ? -lse[(int64_t)head * a.T + row] / a.scale : 0.0f;
-    if (h == 0 && row < at.end) {  // the same starting values for the dk, dv kernel
+    if (part == 0 && h == 0 && row < at.end) {  // the same starting values for the dk, dv kernel
         stats[(int64_t)head * a.T + row] = ls;
         stats[(int64_t)(a.H + head) * a.T + row] = dl;
     }
@@ -449,8 +491,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
         }
         const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int k0 = key0 + 32 * t;
+        for (int t = 0; t < 2 / PARTS; ++t) {
+            const int k0 = key0 + 32 * (t + part);
             if (k0 > row0 + 31) break;
             f32x16 s, dp;
 #pragma unroll
@@ -481,6 +523,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(
     for (int j = 0; j < tiles; j += 2) {
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
+    }
+    if (PARTS > 1) {
+        float *other = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64 + l;
+        __syncthreads();  // the tiles are read
+        if (part == 1) put_tiles<DP / 32>(other, acc);
+        __syncthreads();
+        if (part == 1) return;
+        add_tiles<DP / 32>(acc, 1.0f, other, 1.0f);
     }
     store_rows<DP>(dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
 }
@@ -513,12 +563,16 @@ __device__ __forceinline__ void store_rows_f32(float *y, int64_t ld, int row0, i
 // head, partial results) or of all heads of the group.  The keys stay in LDS and
 // the values in registers: with both in registers the two accumulators leave no
 // room for two waves a SIMD.
-template <int DP, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
+template <int DP, bool SPLIT, int PARTS>
+__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
     const float *__restrict__ stats, const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, KvOut out) {
-    constexpr int kTile = 32;
-    __shared__ __attribute__((aligned(256))) uint16_t ks_[kOwn * DP], qs_[2][kTile * DP], ds_[2][kTile * DP];
+    constexpr int kTile = 32 * PARTS;
+    // the keys and the tiles; at the end of two parts dk and dv on their way from one to the other
+    constexpr int kLds = PARTS > 1 ? 4 * kOwn * DP : kOwn * DP + 4 * kTile * DP;
+    __shared__ __attribute__((aligned(256))) uint16_t lds_[kLds];
+    uint16_t *ks_ = lds_;
+    uint16_t(*qs_)[kTile * DP] = reinterpret_cast<uint16_t(*)[kTile * DP]>(lds_ + kOwn * DP), (*ds_)[kTile * DP] = qs_ + 2;
     __shared__ __attribute__((aligned(16))) float ls_[2][kTile], dl_[2][kTile];
     const int group = a.H / a.Hk, heads = SPLIT ? a.H : a.Hk;
     const int first_head = SPLIT ? head_of(blockIdx.x % a.H, a.H, a.Hk) : (int)(blockIdx.x % a.Hk) * group;
@@ -539,26 +593,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
         }
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
     const int key0 = at.first + 32 * wave, key = key0 + (l & 31);
-    Mover<DP, kTile, true> mq, md;
+    Mover<DP, kTile, kWaves * PARTS, true> mq, md;
     mq.init(a.ldq, a.D);
     md.init(ldo, a.D);
     Reader<DP, true> rd;
-    rd.init();
+    rd.init(32 * part);
     // A tile of rows and their statistics.  Rows past the end are zeros throughout: p = 1
     // there, against do = 0 and q = 0.
     auto fetch = [&](int hd, int r0, int b) {
         mq.load(q + (int64_t)hd * a.D, a.ldq, a.D, r0, at.end, lds_addr(qs_[b]));
         md.load(dout + (int64_t)hd * a.D, ldo, a.D, r0, at.end, lds_addr(ds_[b]));
-        if (wave < 2 && l < kTile) {
+        if (part == 0 && wave < 2 && l < kTile) {
             const __amdgpu_buffer_rsrc_t r = out_rsrc(stats + (int64_t)(wave * a.H + hd) * a.T + r0, (int64_t)(at.end - r0) * 4);
             transfer4(r, lds_addr(wave ? dl_[b] : ls_[b]), l * 4);
         }
     };
     int hd = first_head, r0 = at.first;  // of the tile at hand
     {
-        Mover<DP, kOwn, false> mk;
+        Mover<DP, kOwn, kWaves * PARTS, false> mk;
         mk.init(a.ldk, a.D);
         mk.load(k + (int64_t)kv * a.D, a.ldk, a.D, at.first, at.end, lds_addr(ks_));
     }
@@ -571,7 +626,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.0f;
     const float c = a.scale * kLog2e;
-    uint32_t kt_ = lds_addr(ks_) + 32 * wave * DP * 2;
+    uint32_t kt_ = lds_addr(ks_) + 32 * (wave - part) * DP * 2;  // the reader is 32 part rows ahead
     const int per = (at.end - at.first + kTile - 1) / kTile, tiles = per * (SPLIT ? 1 : group);
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
@@ -583,8 +638,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
         }
         if (j + 1 < tiles) fetch(next_hd, next_r0, 1 - B);
         const uint32_t qt_ = lds_addr(qs_[B]), dt_ = lds_addr(ds_[B]);
-        const uint32_t lt_ = lds_addr(ls_[B]) + 16 * h, et_ = lds_addr(dl_[B]) + 16 * h;
-        const int q0 = r0;
+        const uint32_t lt_ = lds_addr(ls_[B]) + 16 * h + 128 * part, et_ = lds_addr(dl_[B]) + 16 * h + 128 * part;
+        const int q0 = r0 + 32 * part;
         hd = next_hd;
         r0 = next_r0;
         if (q0 + 31 < key0) return;  // these rows all come before the wave's keys
@@ -629,12 +684,22 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
+    if (PARTS > 1) {
+        float *dk = reinterpret_cast<float *>(lds_) + wave * (DP / 2) * 64 + l, *dv = dk + kWaves * (DP / 2) * 64;
+        __syncthreads();  // the tiles are read
+        if (part == 1) put_tiles<DP / 32>(dk, ak);
+        else put_tiles<DP / 32>(dv, av);
+        __syncthreads();
+        if (part == 0) add_tiles<DP / 32>(ak, 1.0f, dk, 1.0f);
+        else add_tiles<DP / 32>(av, 1.0f, dv, 1.0f);
+    }
+    const bool has_k = part == 0, has_v = part == PARTS - 1;
     if (SPLIT) {
-        store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
-        store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
+        if (has_k) store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
+        if (has_v) store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
     } else {
-        store_rows<DP>(out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
-        store_rows<DP>(out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
+        if (has_k) store_rows<DP>(out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
+        if (has_v) store_rows<DP>(out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
     }
 }
 
@@ -670,27 +735,48 @@ bool split_heads(const AttentionShape &a) {
     const double len = a.T / a.S;
     return a.H > a.Hk && len * 131072 > (double)a.T * a.Hk * (len + 1536);
 }
+
+// Two parts where the workgroups (about T H / 128) are no more than the 512 that run
+// at a time with one part, and sequences long enough for the steps saved to pay for
+// the parts' meeting.  Backward, one part / two (us): 1 x 8192 H / Hk 8 / 2 D 128 638 / 491, 2 x 2048 16 / 16 D 64
+// 131 / 97, 1 x 500 32 / 32 D 128 51 / 47; 2 x 256 8 / 8 D 128 33 / 34, 4 x 512 32 / 32 D 64 49 / 56,
+// 1 x 8192 16 / 4 D 128 939 / 966.  Forward, the same: 174 / 154, 43 / 40, 17 / 17; 11 / 13, 18 / 19, 289 / 301.
+bool two_parts(const AttentionShape &a) {
+    const int64_t len = a.T / a.S, rows = (int64_t)a.T * a.H;
+    return len >= 384 && rows <= 65536 && rows <= 80 * len;
+}
 size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
 
-template <int DP>
+template <int DP, int PARTS>
 hipError_t backward(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                     const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout, const int32_t *cu,
                     uint16_t *dq, int64_t lddq, float *stats, const KvOut &out, hipStream_t s) {
+    constexpr int kT = kThreads * PARTS;
     const int slots = slots_of(a);
-    attention_dq_kernel<DP><<<(unsigned)slots * a.H, kThreads, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats,
-                                                                      slots);
+    attention_dq_kernel<DP, PARTS><<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, slots);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!split_heads(a)) {
-        attention_dkv_kernel<DP, false><<<(unsigned)slots * a.Hk, kThreads, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+        attention_dkv_kernel<DP, false, PARTS><<<(unsigned)slots * a.Hk, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
         return hipGetLastError();
     }
-    attention_dkv_kernel<DP, true><<<(unsigned)slots * a.H, kThreads, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+    attention_dkv_kernel<DP, true, PARTS><<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t chunks = (int64_t)a.T * a.Hk * (a.D / 8);
     attention_group_sum_kernel<<<dim3((unsigned)((chunks + kThreads - 1) / kThreads), 2), kThreads, 0, s>>>(a, out);
     return hipGetLastError();
+}
+
+// f with the padded head dimension and the parts as template values.
+template <typename F>
+hipError_t shaped(const AttentionShape &a, F f) {
+    using std::integral_constant;
+    if (a.D <= 64)
+        return two_parts(a) ? f(integral_constant<int, 64>(), integral_constant<int, 2>())
+                            : f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    return two_parts(a) ? f(integral_constant<int, 128>(), integral_constant<int, 2>())
+                        : f(integral_constant<int, 128>(), integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -704,12 +790,11 @@ size_t attention_bwd_bytes(const AttentionShape &a) {
 hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s) {
     const int slots = slots_of(a);
-    const unsigned groups = (unsigned)slots * a.H;
-    if (a.D <= 64)
-        attention_fwd_kernel<64><<<groups, kThreads, 0, s>>>(a, q, k, v, cu, o, res, lse, slots);
-    else
-        attention_fwd_kernel<128><<<groups, kThreads, 0, s>>>(a, q, k, v, cu, o, res, lse, slots);
-    return hipGetLastError();
+    return shaped(a, [&](auto dp, auto parts) {
+        constexpr int kDp = decltype(dp)::value, kParts = decltype(parts)::value;
+        attention_fwd_kernel<kDp, kParts><<<(unsigned)slots * a.H, kThreads * kParts, 0, s>>>(a, q, k, v, cu, o, res, lse, slots);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
@@ -718,8 +803,9 @@ hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, cons
                                 uint16_t *dv, int64_t lddv, void *ws, hipStream_t s) {
     float *stats = static_cast<float *>(ws);
     const KvOut out{dk, dv, lddk, lddv, reinterpret_cast<float *>(static_cast<char *>(ws) + stats_bytes(a))};
-    return a.D <= 64 ? backward<64>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s)
-                     : backward<128>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
+    return shaped(a, [&](auto dp, auto parts) {
+        return backward<decltype(dp)::value, decltype(parts)::value>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
+    });
 }
 
 }  // namespace qnf4

@@ -125,6 +125,32 @@ def test_packed_sequences(d):
     check([200], 260, 2, 2, d, 6, head=1)
 
 
+@pytest.mark.parametrize("lens,h,hk,d", [
+    ([384], 2, 2, 64), ([385], 2, 1, 128), ([449, 703], 2, 2, 128), ([512, 1, 1040], 3, 1, 64), ([1027, 130, 0, 545], 4, 2, 72),
+    ([800], 1, 1, 40), ([480, 480], 2, 2, 112)])
+def test_few_long_sequences(lens, h, hk, d):
+    """Sequences whose tiles two groups of waves share."""
+    check(lens, 7, h, hk, d, len(lens), fused=True, head=5)
+
+
+def test_few_long_sequences_keep_apart():
+    """NaN and infinity in one of them and around them leave the others' bits alone; the same bits on every run."""
+    import bit_nf4_quantized_13_amd as q_
+    say("attention long neighbours")
+    for d in (64, 128):
+        q, k, v, do, starts, cu = make([450, 391, 500], 9, 2, 1, d, 21, fused=True, head=3)
+        clean = q_.qlora_attention_fwd(q, k, v, cu, save_residual=True)
+        grads = q_.qlora_attention_bwd(q, k, v, clean[0], clean[1], do, cu, residual=clean[2])
+        bad = np.r_[0:3, starts[1]:starts[2], starts[3]:q.shape[0]]
+        keep = np.setdiff1d(np.arange(q.shape[0]), bad)
+        for t in (q, k, v, do):
+            t[bad] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1.0] * (d // 4)).cuda().bfloat16()
+        o, lse, res = q_.qlora_attention_fwd(q, k, v, cu, save_residual=True)
+        got = q_.qlora_attention_bwd(q, k, v, o, lse, do, cu, residual=res)
+        assert torch.equal(o[keep], clean[0][keep]) and torch.equal(lse[:, keep], clean[1][:, keep])
+        assert all(torch.equal(s[keep], t[keep]) for s, t in zip(got, grads))
+
+
 def test_many_short_sequences():
     """More sequences than the 64 and the 4096 that one and two steps of the look-up cover."""
     check([1 + i % 7 for i in range(150)], 3, 2, 1, 64, 7)

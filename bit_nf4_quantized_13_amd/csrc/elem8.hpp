@@ -1,8 +1,9 @@
 // Rows of bf16 or fp32 taken 8 consecutive elements at a time, widened to
 // fp32.  A full group is read or written with 16-byte accesses at any element
 // alignment (gfx950 takes unaligned global accesses; an odd row pitch or a
-// view that starts mid-buffer needs no second code path), the last group of a
-// row element by element, so nothing outside the row is touched.
+// view that starts mid-buffer needs no second code path).  Nothing outside the row
+// is touched: the group that its end falls into is stored element by element, and
+// read the same way or (RowLoad) as the row's last 8 elements.
 #pragma once
 #include "common.hpp"
 

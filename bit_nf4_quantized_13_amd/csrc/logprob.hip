@@ -31,6 +31,10 @@
 // most top 256 elements remain, usually some dozen; they are collected in LDS and
 // each counts the larger ones (of thousands of equal ones, the best are taken one
 // by one).
+//
+// Measured, bf16: 2048 x 131071 with 8 alternatives 142 + 9 us for 537 MB, 92 in
+// all without them (5.8 TB/s); one row of 32000 with 5 alternatives 8.0 us;
+// gradient of 4096 x 32000 81 to 92 us for 524 MB.
 #include "elem8.hpp"
 #include "launch.hpp"
 

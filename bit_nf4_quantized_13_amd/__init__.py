@@ -453,16 +453,18 @@ def _rows(t: torch.Tensor, name: str) -> int:
     """The row pitch, in elements, of a device matrix whose rows are dense."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError(f"{name} must be a matrix with dense rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if shape[0] < 2:
+        return shape[1]
+    if strides[0] < shape[1]:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return strides[0]
 
 
 def _shaped(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> torch.Tensor:
-    _dev_tensor(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if _dev_tensor(t, dtype, name).shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -480,7 +482,7 @@ def qlora_layernorm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bia
             _shaped(t, ref.dtype, (n,), name)
     y = _shaped(out, x.dtype, (m, n), "out") if out is not None else torch.empty((m, n), dtype=x.dtype, device=x.device)
     mean = torch.empty(m, dtype=torch.float32, device=x.device) if save_stats else None
-    rstd = torch.empty(m, dtype=torch.float32, device=x.device) if save_stats else None
+    rstd = torch.empty_like(mean) if save_stats else None
     _check(_lib.qlora_layernorm_fwd(x.data_ptr(), kind, m, n, ld, _ptr(weight), _ptr(bias), wkind, float(eps),
                                     y.data_ptr(), _ptr(mean), _ptr(rstd), _stream()), "qlora_layernorm_fwd")
     return y, mean, rstd

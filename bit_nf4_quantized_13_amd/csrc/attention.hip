@@ -238,28 +238,57 @@ __device__ __forceinline__ void load_rows(const uint16_t *x, int64_t ld, int row
     }
 }
 
-// Stores a transposed result (columns 32 dt + tile_row + 4 (l / 32), row l % 32) times f as bf16 rows; res: the residuals.
+// A wave's transposed result (columns 32 dt + tile_row + 4 (l / 32), row l % 32) on its
+// way to memory: a lane holds 4 values of a row here and there, so the tile goes
+// through the wave's own LDS (32 rows of DP bf16, chunks of 16 bytes in an order that
+// depends on the row) and leaves as whole rows (8-byte pieces from the registers cost the
+// forward of 4 x 1024, 32 heads, OLD us against NEW).
 template <int DP>
-__device__ __forceinline__ void store_rows(uint16_t *y, uint16_t *res, int64_t ld, int row0, int end, int D,
+struct RowWriter {
+    static constexpr int kChunks = DP / 8, kRows = 64 / kChunks;
+    typedef u32x2 pair __attribute__((may_alias));
+    typedef u32x4 chunk __attribute__((may_alias));
+    char *lds;
+    static __device__ __forceinline__ int order(int r) { return DP == 128 ? r & 15 : (r >> 1) & 7; }
+    __device__ __forceinline__ void put(int dt, int i, uint32_t w0, uint32_t w1) const {
+        const int l = threadIdx.x & 63, r = l & 31;
+        *reinterpret_cast<pair *>(lds + r * DP * 2 + (((4 * dt + i / 4) ^ order(r)) * 16) + (l >> 5) * 8) = u32x2{w0, w1};
+    }
+    __device__ __forceinline__ void out(uint16_t *y, int64_t ld, int row0, int end, int D) const {
+        const int l = threadIdx.x & 63, c = l % kChunks;
+        asm volatile("" ::: "memory");  // the wave's own writes come first: LDS keeps their order
+#pragma unroll
+        for (int j = 0; j < 32 / kRows; ++j) {
+            const int r = j * kRows + l / kChunks;
+            const u32x4 w = *reinterpret_cast<const chunk *>(lds + r * DP * 2 + ((c ^ order(r)) * 16));
+            if (row0 + r < end && c * 8 < D) *reinterpret_cast<chunk *>(y + (int64_t)(row0 + r) * ld + c * 8) = w;
+        }
+        asm volatile("" ::: "memory");
+    }
+};
+
+// The result times f as bf16 rows; res: what the rounding drops.  lds: the wave's 64 DP bytes.
+template <int DP>
+__device__ __forceinline__ void store_rows(void *lds, uint16_t *y, uint16_t *res, int64_t ld, int row0, int end, int D,
                                            const f32x16 *t, float f) {
-    const int l = threadIdx.x & 63, h = l >> 5, row = row0 + (l & 31);
-    if (row >= end) return;
+    const RowWriter<DP> to{static_cast<char *>(lds)};
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            to.put(dt, i, pack_bf16x2(t[dt][i] * f, t[dt][i + 1] * f), pack_bf16x2(t[dt][i + 2] * f, t[dt][i + 3] * f));
+    to.out(y, ld, row0, end, D);
+    if (!res) return;
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const int c = 32 * dt + tile_row(i) + 4 * h;
-            if (c >= D) continue;
-            const float a = t[dt][i] * f, b = t[dt][i + 1] * f, d = t[dt][i + 2] * f, e = t[dt][i + 3] * f;
-            const uint2 w = make_uint2(pack_bf16x2(a, b), pack_bf16x2(d, e));
-            *reinterpret_cast<uint2 *>(y + (int64_t)row * ld + c) = w;
-            if (res) {
-                const float ra = a - __uint_as_float(w.x << 16), rb = b - __uint_as_float(w.x & 0xFFFF0000u);
-                const float rd = d - __uint_as_float(w.y << 16), re = e - __uint_as_float(w.y & 0xFFFF0000u);
-                *reinterpret_cast<uint2 *>(res + (int64_t)row * ld + c) =
-                    make_uint2(pack_bf16x2(ra, rb), pack_bf16x2(rd, re));
-            }
+            const float a = t[dt][i] * f, b = t[dt][i + 1] * f, c = t[dt][i + 2] * f, d = t[dt][i + 3] * f;
+            const uint32_t w = pack_bf16x2(a, b), x = pack_bf16x2(c, d);
+            to.put(dt, i, pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xFFFF0000u)),
+                   pack_bf16x2(c - __uint_as_float(x << 16), d - __uint_as_float(x & 0xFFFF0000u)));
         }
+    to.out(res, ld, row0, end, D);
 }
 
 // Zeros in the rows [row0, end) of one head, by the whole workgroup.
@@ -402,9 +431,10 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(Atte
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     sum = pair_sum(sum);
+    float *mine = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64;
+    __syncthreads();  // the tiles are read
     if (PARTS > 1) {
-        float *other = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64 + l;
-        __syncthreads();  // the tiles are read
+        float *other = mine + l;
         if (part == 1) {
             put_tiles<DP / 32>(other, acc);
             meet[0][wave * 64 + l] = m;
@@ -418,7 +448,7 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(Atte
         sum = sum * f0 + meet[1][wave * 64 + l] * f1;
         m = top;
     }
-    store_rows<DP>(o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
+    store_rows<DP>(mine, o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
     if (h == 0 && row < at.end) lse[(int64_t)head * a.T + row] = m * a.scale + logf(sum);
 }
 
@@ -527,15 +557,16 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
+    float *mine = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64;
+    __syncthreads();  // the tiles are read
     if (PARTS > 1) {
-        float *other = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64 + l;
-        __syncthreads();  // the tiles are read
+        float *other = mine + l;
         if (part == 1) put_tiles<DP / 32>(other, acc);
         __syncthreads();
         if (part == 1) return;
         add_tiles<DP / 32>(acc, 1.0f, other, 1.0f);
     }
-    store_rows<DP>(dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
+    store_rows<DP>(mine, dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
 }
 
 // Where the dk, dv kernel's results go: the gradients, or with `part` one fp32
@@ -687,9 +718,10 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
+    float *mine = reinterpret_cast<float *>(lds_) + (part * kWaves + wave) * (DP / 2) * 64;
+    __syncthreads();  // the tiles are read
     if (PARTS > 1) {
         float *dk = reinterpret_cast<float *>(lds_) + wave * (DP / 2) * 64 + l, *dv = dk + kWaves * (DP / 2) * 64;
-        __syncthreads();  // the tiles are read
         if (part == 1) put_tiles<DP / 32>(dk, ak);
         else put_tiles<DP / 32>(dv, av);
         __syncthreads();
@@ -701,8 +733,8 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
         if (has_k) store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
         if (has_v) store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
     } else {
-        if (has_k) store_rows<DP>(out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
-        if (has_v) store_rows<DP>(out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
+        if (has_k) store_rows<DP>(mine, out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
+        if (has_v) store_rows<DP>(mine, out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
     }
 }
 

@@ -538,13 +538,13 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
                 s = mfma(rd.rows(kt_, t, ks), qf[ks], s);
                 dp = mfma(rd.rows(vt_, t, ks), df[ks], dp);
             }
-            const bool edge = k0 + 31 > row0;
+            if (k0 + 31 > row0) {  // a branch: most tiles have nothing to mask
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float p = __builtin_amdgcn_exp2f(s[i] * c);
-                if (edge && k0 + tile_row(i) > row - 4 * h) p = 0.0f;
-                s[i] = p * dp[i];
+                for (int i = 0; i < 16; ++i)
+                    if (k0 + tile_row(i) > row - 4 * h) s[i] = -INFINITY;
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
                 const bf16x8 ds = operand_of(s, st);
@@ -694,13 +694,15 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
             s = mfma(rd.rows(qt_, 0, ks), rd.rows(kt_, 0, ks), s);
             dp = mfma(rd.rows(dt_, 0, ks), vf[ks], dp);
         }
-        const bool edge = q0 < key0 + 31;
+        if (q0 < key0 + 31) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (q0 + tile_row(i) < key - 4 * h) s[i] = -INFINITY;
+        }
         u32x4 pw[2], sw[2];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            float p0 = __builtin_amdgcn_exp2f(s[i] * c), p1 = __builtin_amdgcn_exp2f(s[i + 1] * c);
-            if (edge && q0 + tile_row(i) < key - 4 * h) p0 = 0.0f;
-            if (edge && q0 + tile_row(i + 1) < key - 4 * h) p1 = 0.0f;
+            const float p0 = __builtin_amdgcn_exp2f(s[i] * c), p1 = __builtin_amdgcn_exp2f(s[i + 1] * c);
             pw[i / 8][i / 2 % 4] = pack_bf16x2(p0, p1);
             sw[i / 8][i / 2 % 4] = pack_bf16x2(p0 * dp[i], p1 * dp[i + 1]);
         }

@@ -20,7 +20,7 @@
 // workgroup holds its piece of a row in registers, 32 elements a thread: the
 // maximum first, then the exponentials against it, with no running rescale.
 // Rows are cut into chunks of at most 8192 for 256 threads, whose (max, l, sum
-// e^d d) and best candidates go to the workspace, and a wave a row joins them in
+// e^d d) and groups' maxima go to the workspace, and a wave a row joins them in
 // chunk order in a second launch; of few rows, one of up to 32768 elements is a
 // workgroup's of 1024 threads, which writes its results.
 //
@@ -28,13 +28,13 @@
 // 8 threads (2 where a thread has 8 elements) owns up to 256 in a row; the top-th
 // best of these groups by (maximum, then place) bounds the candidates: an element
 // below its maximum, or equal to it in a later group, has top better ones.  So at
-// most top 256 elements remain, usually some dozen; they are collected in LDS and
-// each counts the larger ones (of thousands of equal ones, the best are taken one
-// by one).
+// most top 256 elements remain, usually some dozen (the join reads their groups
+// again, 0.1 to 1 % of the row); they are collected in LDS and each counts the larger
+// ones (of thousands of equal ones, the best are taken one by one).
 //
-// Measured, bf16: 2048 x 131071 with 8 alternatives 142 + 9 us for 537 MB, 92 in
-// all without them (5.8 TB/s); one row of 32000 with 5 alternatives 8.0 us;
-// gradient of 4096 x 32000 81 to 92 us for 524 MB.
+// Measured, bf16: 2048 x 131071 with 8 alternatives 94 + 11 us for 537 MB (the first
+// kernel 5.7 TB/s; 142 + 9 with the chunks' own search for them); one row of 32000 with 5
+// alternatives 8.0 us; gradient of 4096 x 32000 81 to 92 us for 524 MB.
 #include "elem8.hpp"
 #include "launch.hpp"
 
@@ -48,6 +48,7 @@ constexpr int kHeld = kVecs * 8;                  // elements a thread
 constexpr int kChunk = kThreads * kHeld;          // 8192
 constexpr int64_t kWholeRow = kRowThreads * kHeld;  // 32768
 constexpr int kGroupElems = 256;                  // most elements of a group
+constexpr int kChunkGroups = kThreads / 8;        // of a chunk, when its row's best are looked for
 constexpr int kCandBytes = kGroupElems * 12 + kGroupElems / 8 * 4;  // their keys, values and vectors' places
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -90,17 +91,24 @@ struct RowOut {
     float *logp, *entropy, *lse, *top_logp;
     int32_t *top_ids;
 };
+// The target's logit, asked for before the row's sums are known.
+struct Target {
+    bool has;
+    float x;
+};
 template <typename T>
-__device__ __forceinline__ void write_row(const RowOut &o, int64_t row, const T *xr, int64_t V, float mx, float base,
-                                          float l, float a) {
+__device__ __forceinline__ Target target_of(const RowOut &o, int64_t row, const T *xr, int64_t V) {
+    const int64_t t = o.logp ? o.targets[row] : -1;
+    const bool has = t >= 0 && t < V;
+    return Target{has, load1(xr + (has ? t : 0))};
+}
+__device__ __forceinline__ void write_row(const RowOut &o, int64_t row, const Target &t, float mx, float base, float l,
+                                          float a) {
     const bool none = none_left(mx, l);
     const float log_l = logf(l);
     if (o.lse) o.lse[row] = none ? -INFINITY : base + log_l;
     if (o.entropy) o.entropy[row] = none ? 0.0f : log_l - a / l;
-    if (o.logp) {
-        const int64_t t = o.targets[row];
-        o.logp[row] = t < 0 || t >= V ? 0.0f : none ? -INFINITY : load1(xr + t) - base - log_l;
-    }
+    if (o.logp) o.logp[row] = !t.has ? 0.0f : none ? -INFINITY : t.x - base - log_l;
 }
 
 // Two sums over the workgroup, on every thread, in wave order.
@@ -121,13 +129,13 @@ __device__ __forceinline__ void group_totals(float &l, float &a, float (*red)[TH
     }
 }
 
-// One piece of a row.  ROW: the whole row, its results to `out`; otherwise chunk
-// blockIdx.x % chunks of row blockIdx.x / chunks, its sums to stats and best.
-// LDS beyond the static: top kCandBytes.
+// One piece of a row.  ROW: the whole row, its results to `out` (LDS beyond the static:
+// top kCandBytes); otherwise chunk blockIdx.x % chunks of row blockIdx.x / chunks, its
+// sums to stats and its groups' maxima.
 template <typename T, bool TOP, int THREADS, bool ROW>
 __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restrict__ x, int64_t V, int64_t ld,
                                                                 int chunks, int64_t len, int top,
-                                                                float *__restrict__ stats, u64 *__restrict__ best,
+                                                                float *__restrict__ stats, float *__restrict__ maxima,
                                                                 RowOut out) {
     __shared__ float red[3][THREADS / 64];
     __shared__ float gmax[TOP ? THREADS / 2 : 1];
@@ -139,7 +147,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     const int left = (int)(V - c0 < len ? V - c0 : len);
     const T *xr = x + row * ld + c0;
     // groups of gt threads, nv vectors of 8 a thread, side by side
-    const int nv = (left + THREADS * 8 - 1) / (THREADS * 8), gt = nv == 1 ? 2 : 8, gshift = nv == 1 ? 1 : 3;
+    const int nv = (int)((len + THREADS * 8 - 1) / (THREADS * 8)), gt = nv == 1 ? 2 : 8, gshift = nv == 1 ? 1 : 3;
     const int group = tid >> gshift, per = 8 * nv * gt, groups = (left + per - 1) / per;
     const int first = group * per + (tid & (gt - 1)) * 8, step = 8 * gt;
     F8 v[kVecs];
@@ -147,6 +155,8 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     auto at = [&](int i) { return i < nv ? first + i * step : left; };
     RowLoad<T, kVecs> in_flight;
     in_flight.request(xr, left, at);
+    Target target{};
+    if (ROW && tid == 0) target = target_of(out, row, xr, V);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = in_flight.get(xr, left, at, i, -INFINITY);
 #pragma unroll
@@ -162,7 +172,10 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
             g = fmaxf(g, dpp_or<0x4E, 0xF>(g, g));
             g = fmaxf(g, dpp_or<0x141, 0xF>(g, g));
         }
-        if ((tid & (gt - 1)) == 0) gmax[group] = g;
+        if ((tid & (gt - 1)) == 0) {
+            if (ROW) gmax[group] = g;
+            else maxima[(int64_t)blockIdx.x * kChunkGroups + group] = g;
+        }
         if (tid == 0) {
             nvec = ncand = thr_group = 0;
         }
@@ -173,7 +186,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     mx = red[2][0];
 #pragma unroll
     for (int i = 1; i < THREADS / 64; ++i) mx = fmaxf(mx, red[2][i]);
-    if (TOP && tid < groups && groups >= top) {
+    if (TOP && ROW && tid < groups && groups >= top) {
         const float g = gmax[tid];
         int better = 0;
 #pragma unroll 8
@@ -226,7 +239,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     a *= kLn2;
     if (tid == 0) {
         if (ROW) {
-            write_row(out, row, xr, V, mx, base, l, a);
+            write_row(out, row, target, mx, base, l, a);
         } else {
             float *o = stats + (int64_t)blockIdx.x * 4;
             o[0] = mx;
@@ -234,7 +247,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
             o[2] = a;
         }
     }
-    if (!TOP) return;
+    if (!TOP || !ROW) return;
     const bool all = groups < top;       // fewer groups than places: every element is a candidate
     const float thr = gmax[thr_group];
     const bool in = group <= thr_group;  // of groups with the threshold's maximum, these hold candidates
@@ -251,7 +264,6 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
         *reinterpret_cast<f32x4 *>(vals + 8 * j + 4) = f32x4{v[i].v[4], v[i].v[5], v[i].v[6], v[i].v[7]};
     }
     __syncthreads();
-    u64 *list = ROW ? nullptr : best + (int64_t)blockIdx.x * top;
     for (int i = tid; i < 8 * nvec; i += THREADS) {
         const float x1 = vals[i];
         const int c = at_c[i >> 3] + (i & 7);
@@ -261,12 +273,8 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     const int n = ncand;
     const float log_l = logf(l);
     auto place = [&](int rank, u64 k) {
-        if (ROW) {
-            out.top_logp[row * top + rank] = none_left(mx, l) ? -INFINITY : key_value(k) - base - log_l;
-            out.top_ids[row * top + rank] = (int32_t)key_index(k);
-        } else {
-            list[rank] = k;
-        }
+        out.top_logp[row * top + rank] = none_left(mx, l) ? -INFINITY : key_value(k) - base - log_l;
+        out.top_ids[row * top + rank] = (int32_t)key_index(k);
     };
     if (n <= THREADS) {
         if (tid < n) {
@@ -293,17 +301,61 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
             __syncthreads();
         }
     }
-    for (int i = n + tid; i < top; i += THREADS) place(i, 0);  // a chunk of fewer elements, or NaN
+    for (int i = n + tid; i < top; i += THREADS) place(i, 0);  // NaN are none
+}
+
+// Four consecutive elements as they are in memory.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+__device__ __forceinline__ u32x2 raw4(const uint16_t *p) { return *reinterpret_cast<const u32x2_any *>(p); }
+__device__ __forceinline__ u32x4 raw4(const float *p) { return *reinterpret_cast<const u32x4_any *>(p); }
+__device__ __forceinline__ f32x4 widen4(u32x2 w) {
+    return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xFFFF0000u)};
+}
+__device__ __forceinline__ f32x4 widen4(u32x4 w) { return __builtin_bit_cast(f32x4, w); }
+
+// Largest over the wave, on every lane, without a trip through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = dpp_max<0x111, 0xF>(v);  // the steps of wave_max
+    v = dpp_max<0x112, 0xF>(v);
+    v = dpp_max<0x114, 0xF>(v);
+    v = dpp_max<0x118, 0xF>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ u64 wave_max_key(u64 k) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) k = max_key(k, __shfl_xor(k, o));
+    return k;
 }
 
 // One wave a row: the chunks' sums against the row's maximum, lane i holding
-// chunk i, and the chunks' best lists (descending) merged from their heads.
-template <typename T>
+// chunk i.  The best MOST at most (0: none are asked for): the top best groups by
+// (maximum, then place), KEYS a lane, hold them; these groups, 4 elements a lane
+// each, are read again.  LDS: top kGroupElems keys.
+template <typename T, int KEYS, int MOST>
 __global__ __launch_bounds__(64) void logprob_join_kernel(const T *__restrict__ x, int64_t V, int64_t ld, int chunks,
-                                                          const float *__restrict__ stats, const u64 *__restrict__ best,
-                                                          int top, RowOut out) {
+                                                          int64_t len, const float *__restrict__ stats,
+                                                          const float *__restrict__ maxima, int top, RowOut out) {
+    extern __shared__ __attribute__((aligned(16))) u64 cand[];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x;
+    const T *xr = x + row * ld;
+    const Target target = target_of(out, row, xr, V);
+    const int total = chunks * kChunkGroups;
+    float g[KEYS];
+    if (MOST > 0) {
+        const float *gm = maxima + row * total;
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) g[i] = gm[min(i * 64 + lane, total - 1)];
+    }
     const bool mine = lane < chunks;
     const float *s = stats + (row * chunks + lane) * 4;
     const float m = mine ? s[0] : -INFINITY, mx = wave_max(m), base = mx == -INFINITY ? 0.0f : mx;
@@ -315,24 +367,90 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T *__restrict__ 
     }
     l = wave_sum(l);
     a = wave_sum(a);
-    if (lane == 0) write_row(out, row, x + row * ld, V, mx, base, l, a);
-    if (top == 0) return;
-    const float log_l = logf(l);
-    const u64 *list = best + (row * chunks + lane) * top;
-    int at = 0;
-    u64 head = mine ? list[0] : 0;
-    for (int i = 0; i < top; ++i) {
-        u64 k = head;
+    if (lane == 0) write_row(out, row, target, mx, base, l, a);
+    if (MOST > 0 && none_left(mx, l)) {  // all equal: the lowest indices, without the search
+        if (lane < top) {
+            out.top_logp[row * top + lane] = -INFINITY;
+            out.top_ids[row * top + lane] = lane;
+        }
+    } else if constexpr (MOST > 0) {
+        const int per = (int)((len + kThreads * 8 - 1) / (kThreads * 8)) * 64;
+        uint32_t up[KEYS];  // ascending with the maximum; 0: no group, or taken
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) k = max_key(k, __shfl_xor(k, o));
-        if (head == k && k != 0) {
-            ++at;
-            head = at < top ? list[at] : 0;
+        for (int i = 0; i < KEYS; ++i) {
+            const int n = i * 64 + lane, c = n / kChunkGroups, first = n % kChunkGroups * per;
+            up[i] = n < total && c * len + first < V && first < len ? (uint32_t)(key_of(g[i], 0) >> 32) : 0;
         }
-        if (lane == 0) {
-            out.top_logp[row * top + i] = none_left(mx, l) ? -INFINITY : key_value(k) - base - log_l;
-            out.top_ids[row * top + i] = (int32_t)key_index(k);
+        uint32_t best = 0;
+        int chosen = 0, number = 0;  // lane i: the i-th best group
+        for (int i = 0; i < top; ++i) {
+            uint32_t own = 0, place = 0;
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j) own = up[j] > own ? up[j] : own;
+            own = wave_max_u32(own);
+            if (own == 0) break;
+            best = own;
+#pragma unroll
+            for (int j = KEYS - 1; j >= 0; --j) place = up[j] == best ? ~(uint32_t)(j * 64 + lane) : place;
+            place = ~wave_max_u32(place);  // the first of equal ones
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j) up[j] = j * 64 + lane == (int)place ? 0 : up[j];
+            if (lane == i) chosen = (int)place;
+            ++number;
         }
+        const float thr = number < top ? -INFINITY : key_value((u64)best << 32);  // fewer groups than places: all count
+        decltype(raw4((const T *)nullptr)) raw[MOST];
+        int at[MOST], left[MOST];
+        int64_t c0[MOST];
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {  // all requested before the first is used
+            const int n = __builtin_amdgcn_readlane(chosen, i < number ? i : 0), c = n / kChunkGroups;
+            c0[i] = c * len;
+            left[i] = (int)(V - c0[i] < len ? V - c0[i] : len);
+            at[i] = n % kChunkGroups * per + lane * 4;
+            raw[i] = raw4(xr + c0[i] + min(at[i], left[i] - 4));  // a chunk has thousands of elements
+        }
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            if (i >= number) continue;
+            f32x4 v = widen4(raw[i]);
+            const bool cut = at[i] + 4 > left[i];
+            if (__ballot(cut) && cut) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = at[i] + e < left[i] ? load1(xr + c0[i] + at[i] + e) : NAN;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = v[e] >= thr && lane * 4 < per;
+                const u64 who = __ballot(in);
+                if (who == 0) continue;
+                if (in) cand[n + __popcll(who & (((u64)1 << lane) - 1))] = key_of(v[e], (uint32_t)(c0[i] + at[i] + e));
+                n += __popcll(who);
+            }
+        }
+        __syncthreads();
+        const float log_l = logf(l);
+        auto place = [&](int rank, u64 k) {
+            out.top_logp[row * top + rank] = key_value(k) - base - log_l;
+            out.top_ids[row * top + rank] = (int32_t)key_index(k);
+        };
+        if (n <= 64) {
+            const u64 k = lane < n ? cand[lane] : 0;
+            int larger = 0;
+            for (int j = 0; j < n; ++j) larger += cand[j] > k;
+            if (lane < n && larger < top) place(larger, k);
+        } else {  // many equal logits: one after the other, each the largest below the last
+            u64 last = ~(u64)0;
+            for (int i = 0; i < top; ++i) {
+                u64 k = 0;
+#pragma unroll 8
+                for (int j = lane; j < n; j += 64) k = cand[j] < last ? max_key(k, cand[j]) : k;
+                last = wave_max_key(k);
+                if (lane == 0) place(i, last);
+            }
+        }
+        for (int i = n + lane; i < top; i += 64) place(i, 0);  // NaN are none
     }
 }
 
@@ -404,16 +522,16 @@ __global__ __launch_bounds__(kThreads) void logprob_bwd_kernel(const T *x, int64
 }  // namespace
 
 // Rows that go whole to a workgroup each, with one launch and no join: those of one chunk,
-// and longer ones where there are no more of them than CUs (one row of 32000 with 5
-// alternatives 9.7 against 11.6 us, 128 rows 10.9 against 12.6); with more, the chunks'
-// smaller workgroups overlap better (4096 rows 84 against 147 us).
+// and longer ones where there are no more of them than CUs (bf16, 32000 logits, 5 alternatives: one
+// row 8.7 us against 9.3, 256 rows 9.6 against 11.9); with more, the chunks' smaller
+// workgroups overlap better (512 rows 15.2 against 18.0, 4096 rows 57 against 128).
 bool whole_rows(int64_t M, int64_t V) { return V <= kChunk || (M <= 256 && V <= kWholeRow); }
 
 size_t logprob_stats_bytes(int64_t M, int64_t V) {
     return whole_rows(M, V) ? 0 : sizeof(float) * 4 * (size_t)M * cut_of(V).chunks;
 }
 size_t logprob_best_bytes(int64_t M, int64_t V, int top) {
-    return whole_rows(M, V) ? 0 : sizeof(u64) * (size_t)top * (size_t)M * cut_of(V).chunks;
+    return whole_rows(M, V) || top == 0 ? 0 : sizeof(float) * kChunkGroups * (size_t)M * cut_of(V).chunks;
 }
 int64_t logprob_groups(int64_t M, int64_t V) { return M * cut_of(V).chunks; }
 
@@ -421,7 +539,6 @@ hipError_t launch_logprob_fwd(const void *x, bool f32, int64_t M, int64_t V, int
                               int top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
                               float *stats, void *best, hipStream_t s) {
     const RowOut out{targets, logp, entropy, lse, top_logp, top_ids};
-    const size_t lds = (size_t)top * kCandBytes;  // up to 50 KiB
     auto run = [&](auto *p) {
         using T = std::remove_pointer_t<decltype(p)>;
         const T *xt = (const T *)x;
@@ -434,12 +551,16 @@ hipError_t launch_logprob_fwd(const void *x, bool f32, int64_t M, int64_t V, int
                                          : logprob_piece_kernel<T, false, kRowThreads, true>
                        : top > 0 ? logprob_piece_kernel<T, true, kThreads, false>
                                  : logprob_piece_kernel<T, false, kThreads, false>;
-        kernel<<<groups, whole && !small ? kRowThreads : kThreads, lds, s>>>(xt, V, ld, cut.chunks, whole ? V : cut.len, top,
-                                                                           stats, (u64 *)best, out);
-        if (whole) return hipGetLastError();
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        logprob_join_kernel<T><<<(unsigned)M, 64, 0, s>>>(xt, V, ld, cut.chunks, stats, (const u64 *)best, top, out);
+        kernel<<<groups, whole && !small ? kRowThreads : kThreads, whole ? (size_t)top * kCandBytes : 0, s>>>(  // up to 50 KiB
+            xt, V, ld, cut.chunks, whole ? V : cut.len, top, stats, (float *)best, out);
+        hipError_t e = hipGetLastError();
+        if (whole || e != hipSuccess) return e;
+        const bool wide = cut.chunks > 16;
+        auto *join = top == 0   ? logprob_join_kernel<T, 1, 0>
+                     : top <= 8 ? wide ? logprob_join_kernel<T, 32, 8> : logprob_join_kernel<T, 8, 8>
+                                : wide ? logprob_join_kernel<T, 32, 16> : logprob_join_kernel<T, 8, 16>;
+        join<<<(unsigned)M, 64, sizeof(u64) * kGroupElems * (size_t)top, s>>>(xt, V, ld, cut.chunks, cut.len, stats,
+                                                                              (const float *)best, top, out);
         return hipGetLastError();
     };
     return f32 ? run((float *)nullptr) : run((uint16_t *)nullptr);

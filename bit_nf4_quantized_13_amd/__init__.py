@@ -673,6 +673,7 @@ class AdamWPlan:
         self.count = count
         self.table = (_CAdamWTensor * count)()
         self.tensors = (params, grads, m, v, m_scales, v_scales, masters)
+        self.sizes = [p.numel() for p in params]
         for i, (p, g, mi, vi, ms, vs, w) in enumerate(zip(*self.tensors)):
             n = p.numel()
             for t, dtype, size, name in ((p, params[0].dtype, n, "params"), (g, grads[0].dtype, n, "grads"),
@@ -714,9 +715,11 @@ def qlora_adamw_moments(plan: AdamWPlan, m_out=None, v_out=None):
                                                      for t in plan.tensors[2]]
         if len(ts) != plan.count:
             raise ValueError(f"{plan.count} tensors and {len(ts)} {name}")
-        for i, (t, c) in enumerate(zip(ts, plan.tensors[2])):
-            if _dev_tensor(t, torch.float32, f"{name}[{i}]").numel() != c.numel():
-                raise ValueError(f"{name}[{i}] must have {c.numel()} elements")
+        for i, (t, n) in enumerate(zip(ts, plan.sizes)):
+            if t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.numel() == n:
+                continue
+            _dev_tensor(t, torch.float32, f"{name}[{i}]")
+            raise ValueError(f"{name}[{i}] must have {n} elements, got {t.numel()}")
         outs.append(ts)
     ptrs = [(_P * plan.count)(*[t.data_ptr() for t in ts]) for ts in outs]
     _check(_lib.qlora_adamw_moments(plan.table, plan.count, ptrs[0], ptrs[1], _stream()), "qlora_adamw_moments")

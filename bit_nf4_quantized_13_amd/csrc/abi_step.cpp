@@ -257,10 +257,9 @@ int qlora_adamw_moments(const qlora_adamw_tensor *tensors, int32_t count, float 
         if (!aligned(m_out[i], 4) || !aligned(v_out[i], 4)) return QLORA_EALIGN;
     }
     (void)hipGetLastError();
-    constexpr int kBatch = 48;  // tensors handed on at a time, from the stack
-    AdamwTensor batch[kBatch];
-    for (int32_t i = 0; i < count; i += kBatch) {
-        const int n = count - i < kBatch ? count - i : kBatch;
+    AdamwTensor batch[kMaxAdamwTensors];  // a launch's tensors, handed on from the stack
+    for (int32_t i = 0; i < count; i += kMaxAdamwTensors) {
+        const int n = count - i < kMaxAdamwTensors ? count - i : kMaxAdamwTensors;
         for (int j = 0; j < n; ++j) {
             const qlora_adamw_tensor &t = tensors[i + j];
             batch[j] = AdamwTensor{m_out[i + j], v_out[i + j], t.m, t.v, t.m_scale, t.v_scale, nullptr, t.n};

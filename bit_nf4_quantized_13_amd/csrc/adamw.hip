@@ -17,9 +17,9 @@
 // Bound: HBM, 24 bytes an element with fp32 states, 12 with 8-bit states (bf16
 // p, fp32 g).  Each thread takes 8 consecutive elements of every array (16-byte
 // accesses), a block of 256 is half a wave, its maxima 5 lane exchanges.
-// Tensors go to the kernel as arguments, up to kMaxTensors a launch: nothing
+// Tensors go to the kernel as arguments, up to kMaxAdamwTensors a launch: nothing
 // about them is kept anywhere between calls.  Measured: 20 M elements in 56 tensors,
-// 8-bit states, 45 us (12.06 bytes each: 5.3 TB/s), their moments 40 us (10.06 bytes each);
+// 8-bit states, 44 us (12.06 bytes each: 5.5 TB/s), their moments 34 us (10.06 bytes each);
 // 65,536 elements with fp32 states 3.6 us.
 #include "elem8.hpp"
 #include "launch.hpp"
@@ -27,13 +27,12 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kMaxTensors = 59;        // with the list's heads and the rates, 4 KiB of kernel arguments
 constexpr int kThreads = 256;
 constexpr int kChunk = kThreads * 8;   // elements a workgroup takes
 
 struct TensorList {
-    AdamwTensor t[kMaxTensors];
-    uint32_t first[kMaxTensors + 1];  // the tensors' first workgroups
+    AdamwTensor t[kMaxAdamwTensors];
+    uint32_t first[kMaxAdamwTensors + 1];  // the tensors' first workgroups
     int count;
 };
 
@@ -267,7 +266,7 @@ hipError_t in_lists(const AdamwTensor *t, int count, F f) {
     uint32_t wgs = 0;
     for (int i = 0; i <= count; ++i) {
         const uint32_t need = i < count ? (uint32_t)((t[i].n + kChunk - 1) / kChunk) : 0;
-        if (list.count > 0 && (i == count || list.count == kMaxTensors || wgs + need > kMaxAdamwGroups)) {
+        if (list.count > 0 && (i == count || list.count == kMaxAdamwTensors || wgs + need > kMaxAdamwGroups)) {
             list.first[list.count] = wgs;
             f(list, wgs);
             const hipError_t e = hipGetLastError();

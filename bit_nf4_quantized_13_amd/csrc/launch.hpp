@@ -215,6 +215,7 @@ struct AdamwHyper {
     float grad_scale;
 };
 constexpr int64_t kMaxAdamwElems = int64_t(1) << 40;  // of one tensor
+constexpr int kMaxAdamwTensors = 59;                // of a launch: with the rates 4 KiB of kernel arguments
 constexpr uint32_t kMaxAdamwGroups = 1u << 30;        // workgroups of a launch
 // t, on the host, is read before the call returns.
 hipError_t launch_adamw(const AdamwTensor *t, int count, bool p_f32, bool g_f32, bool bits8, bool master,

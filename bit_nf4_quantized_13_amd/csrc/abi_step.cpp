@@ -13,8 +13,9 @@ using namespace qnf4;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;  // workgroups of a launch
-constexpr int64_t kMaxNormWidth = int64_t(1) << 30;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxNormWidth = int64_t(1) << 26;   // a launch over its columns stays below 2^32 threads
+constexpr int64_t kMaxGroups = (int64_t(1) << 23) - 1;  // workgroups of up to 512 threads of a launch: the same
 
 bool known_type(int32_t t) { return t == QLORA_BF16 || t == QLORA_F32; }
 uintptr_t type_bytes(int32_t t) { return t == QLORA_F32 ? 4 : 2; }
@@ -52,7 +53,7 @@ int check_attention(const qlora_attention_shape *s, AttentionShape *a) {
     if (st == QLORA_OK) st = check_pitch(s->ldv, narrow);
     if (st != QLORA_OK) return st;
     *a = AttentionShape{(int)s->T, s->sequences, s->heads, s->kv_heads, s->dim, s->ldq, s->ldk, s->ldv, s->scale};
-    return attention_groups(*a) <= kMaxRows ? QLORA_OK : QLORA_ENOTSUP;
+    return attention_groups(*a) <= kMaxGroups ? QLORA_OK : QLORA_ENOTSUP;
 }
 
 int check_logits(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld) {

@@ -214,9 +214,9 @@ struct AdamwHyper {
     float eps, decay, step_size, v_correction;  // 1 - lr wd, lr / (1 - b1^t), (1 - b2^t)^-1/2
     float grad_scale;
 };
-constexpr int64_t kMaxAdamwElems = int64_t(1) << 40;  // of one tensor
+constexpr int64_t kMaxAdamwElems = int64_t(1) << 34;  // of one tensor
 constexpr int kMaxAdamwTensors = 59;                // of a launch: with the rates 4 KiB of kernel arguments
-constexpr uint32_t kMaxAdamwGroups = 1u << 30;        // workgroups of a launch
+constexpr uint32_t kMaxAdamwGroups = (1u << 24) - 1;  // workgroups of a launch: its threads stay below 2^32
 // t, on the host, is read before the call returns.
 hipError_t launch_adamw(const AdamwTensor *t, int count, bool p_f32, bool g_f32, bool bits8, bool master,
                         const AdamwHyper &h, hipStream_t s);

@@ -39,6 +39,7 @@ constexpr int kMaxPartials = 256;      // its partial rows: one workgroup a CU (
 // less to wait for, is as fast or faster with a workgroup a row (4096 x 8192: 29 us against 35).
 constexpr int kRowThreads = 512;
 constexpr int kMaxRowGroups = 512;
+constexpr int64_t kLaunchRows = 1 << 21;  // of a launch with a workgroup a row: its threads stay below 2^32
 constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
 
 // Sum of v over the TPR threads of a row group (TPR a multiple of 64); every
@@ -385,8 +386,13 @@ hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, 
             return hipGetLastError();
         });
     } else {
-        norm_bwd_stream_kernel<T, W><<<(unsigned)M, kStreamThreads, 0, s>>>(x, dy, n, ldx, mean, rstd, w, dx);
-        e = hipGetLastError();
+        e = hipSuccess;
+        for (int64_t r = 0; r < M && e == hipSuccess; r += kLaunchRows) {
+            const int64_t rows = M - r < kLaunchRows ? M - r : kLaunchRows;
+            norm_bwd_stream_kernel<T, W><<<(unsigned)rows, kStreamThreads, 0, s>>>(x + r * ldx, dy + r * n, n, ldx, mean + r, rstd + r,
+                                                                                  w, dx + r * n);
+            e = hipGetLastError();
+        }
     }
     if (grad && !fused && e == hipSuccess) {
         parts = M < kMaxPartials ? (int)M : kMaxPartials;
@@ -417,7 +423,13 @@ hipError_t launch_layernorm_fwd(const void *x, bool x_f32, int64_t M, int64_t n,
     return typed(x_f32, w_f32, [&](auto *tx, auto *tw) {
         using T = std::remove_pointer_t<decltype(tx)>;
         using W = std::remove_pointer_t<decltype(tw)>;
-        return norm_fwd<T, W>((const T *)x, M, n, ldx, (const W *)w, (const W *)b, eps, (T *)y, mean, rstd, s);
+        for (int64_t r = 0; r < M; r += kLaunchRows) {
+            const hipError_t e = norm_fwd<T, W>((const T *)x + r * ldx, M - r < kLaunchRows ? M - r : kLaunchRows, n, ldx,
+                                                (const W *)w, (const W *)b, eps, (T *)y + r * n, mean ? mean + r : nullptr,
+                                                rstd ? rstd + r : nullptr, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     });
 }
 

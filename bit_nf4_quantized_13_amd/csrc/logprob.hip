@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kThreads = 256;                     // of a chunk, and of the gradient
 constexpr int kRowThreads = 1024;                 // of a whole row
+constexpr int64_t kLaunchGroups = 1 << 23;        // workgroups of a launch: its threads stay below 2^32
 constexpr int kVecs = 4;                          // groups of 8 a thread
 constexpr int kHeld = kVecs * 8;                  // elements a thread
 constexpr int kChunk = kThreads * kHeld;          // 8192
@@ -538,30 +539,38 @@ int64_t logprob_groups(int64_t M, int64_t V) { return M * cut_of(V).chunks; }
 hipError_t launch_logprob_fwd(const void *x, bool f32, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
                               int top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
                               float *stats, void *best, hipStream_t s) {
-    const RowOut out{targets, logp, entropy, lse, top_logp, top_ids};
+    const bool whole = whole_rows(M, V), small = V <= kChunk;
+    const Cut cut = whole ? Cut{1, V} : cut_of(V);
     auto run = [&](auto *p) {
         using T = std::remove_pointer_t<decltype(p)>;
-        const T *xt = (const T *)x;
-        const Cut cut = cut_of(V);
-        const bool whole = whole_rows(M, V), small = V <= kChunk;
-        const unsigned groups = (unsigned)(whole ? M : M * cut.chunks);
         auto *kernel = whole ? small ? top > 0 ? logprob_piece_kernel<T, true, kThreads, true>
                                                : logprob_piece_kernel<T, false, kThreads, true>
                                : top > 0 ? logprob_piece_kernel<T, true, kRowThreads, true>
                                          : logprob_piece_kernel<T, false, kRowThreads, true>
                        : top > 0 ? logprob_piece_kernel<T, true, kThreads, false>
                                  : logprob_piece_kernel<T, false, kThreads, false>;
-        kernel<<<groups, whole && !small ? kRowThreads : kThreads, whole ? (size_t)top * kCandBytes : 0, s>>>(  // up to 50 KiB
-            xt, V, ld, cut.chunks, whole ? V : cut.len, top, stats, (float *)best, out);
-        hipError_t e = hipGetLastError();
-        if (whole || e != hipSuccess) return e;
         const bool wide = cut.chunks > 16;
         auto *join = top == 0   ? logprob_join_kernel<T, 1, 0>
                      : top <= 8 ? wide ? logprob_join_kernel<T, 32, 8> : logprob_join_kernel<T, 8, 8>
                                 : wide ? logprob_join_kernel<T, 32, 16> : logprob_join_kernel<T, 8, 16>;
-        join<<<(unsigned)M, 64, sizeof(u64) * kGroupElems * (size_t)top, s>>>(xt, V, ld, cut.chunks, cut.len, stats,
-                                                                              (const float *)best, top, out);
-        return hipGetLastError();
+        const int threads = whole && !small ? kRowThreads : kThreads;
+        const size_t lds = whole ? (size_t)top * kCandBytes : 0;  // up to 50 KiB
+        const int64_t most = kLaunchGroups / cut.chunks;          // rows of a launch
+        for (int64_t r = 0; r < M; r += most) {
+            const unsigned rows = (unsigned)(M - r < most ? M - r : most);
+            const T *xr = (const T *)x + r * ld;
+            auto from = [&](auto *q, int64_t each) { return q ? q + r * each : nullptr; };
+            const RowOut out{from(targets, 1), from(logp, 1), from(entropy, 1), from(lse, 1), from(top_logp, top), from(top_ids, top)};
+            kernel<<<rows * cut.chunks, threads, lds, s>>>(xr, V, ld, cut.chunks, cut.len, top, stats, (float *)best, out);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            if (whole) continue;
+            join<<<rows, 64, sizeof(u64) * kGroupElems * (size_t)top, s>>>(xr, V, ld, cut.chunks, cut.len, stats,
+                                                                          (const float *)best, top, out);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     };
     return f32 ? run((float *)nullptr) : run((uint16_t *)nullptr);
 }
@@ -571,14 +580,21 @@ hipError_t launch_logprob_bwd(const void *x, bool f32, int64_t M, int64_t V, int
                               int64_t ldd, hipStream_t s) {
     const Cut cut = cut_of(V);
     const int split = x == dx ? 1 : cut.chunks;
-    const unsigned groups = (unsigned)(M * split);
-    if (f32)
-        logprob_bwd_kernel<float><<<groups, kThreads, 0, s>>>((const float *)x, V, ld, split, cut.chunks, cut.len,
-                                                              targets, lse, entropy, dlogp, dent, (float *)dx, ldd);
-    else
-        logprob_bwd_kernel<uint16_t><<<groups, kThreads, 0, s>>>((const uint16_t *)x, V, ld, split, cut.chunks, cut.len,
-                                                                 targets, lse, entropy, dlogp, dent, (uint16_t *)dx, ldd);
-    return hipGetLastError();
+    const int64_t most = kLaunchGroups / split;  // rows of a launch
+    auto run = [&](auto *p) {
+        using T = std::remove_pointer_t<decltype(p)>;
+        for (int64_t r = 0; r < M; r += most) {
+            const unsigned rows = (unsigned)(M - r < most ? M - r : most);
+            auto from = [&](auto *q) { return q ? q + r : nullptr; };
+            logprob_bwd_kernel<T><<<rows * split, kThreads, 0, s>>>((const T *)x + r * ld, V, ld, split, cut.chunks, cut.len,
+                                                                   from(targets), lse + r, from(entropy), from(dlogp),
+                                                                   from(dent), (T *)dx + r * ldd, ldd);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    };
+    return f32 ? run((float *)nullptr) : run((uint16_t *)nullptr);
 }
 
 }  // namespace qnf4

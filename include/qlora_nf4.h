@@ -393,7 +393,7 @@ int qlora_adapter_unmerge(const qlora_bf16 *W_in, int64_t d, int64_t k, const ql
  *   y       device [M x n] of x_type, dense, written
  *   mean, rstd  device fp32 [M], written, or NULL
  * Errors: QLORA_EINVAL (null pointer, size <= 0, ldx < n, eps), QLORA_ENOTSUP
- * (unknown type, M >= 2^31, n > 2^30), QLORA_EALIGN (a pointer not aligned to
+ * (unknown type, M >= 2^31, n > 2^26), QLORA_EALIGN (a pointer not aligned to
  * its element).
  */
 int qlora_layernorm_fwd(const void *x, int32_t x_type, int64_t M, int64_t n, int64_t ldx, const void *weight,
@@ -556,7 +556,7 @@ typedef struct {
  * and its block zeros).  Zeroed codes and scales are the states at the start.
  * Errors: QLORA_EINVAL (null pointer, n < 0, step < 1, a rate out of range,
  * master without use_master or the reverse, use_master with fp32 param),
- * QLORA_ENOTSUP (unknown type, n > 2^40), QLORA_EALIGN.
+ * QLORA_ENOTSUP (unknown type, n > 2^34), QLORA_EALIGN.
  */
 int qlora_adamw_step(const qlora_adamw_tensor *tensors, int32_t count, const qlora_adamw_config *config,
                      void *stream);

@@ -55,6 +55,32 @@ def test_logprob_past_2_31_elements(lib):
     assert torch.equal(got[-1000:], want) and torch.equal(got[35_000:36_000], want)
 
 
+def test_more_rows_than_one_launch_takes(lib):
+    """A launch's threads are fewer than 2^32: rows beyond are launched after one another."""
+    say("layernorm 2^26 rows")
+    m, n = (1 << 26) + 5, 8
+    x = torch.randn(1001, n, device="cuda").bfloat16().repeat(m // 1001 + 1, 1)[:m].contiguous()
+    y, mean, rstd = lib.qlora_layernorm_fwd(x)
+    y1, mean1, rstd1 = lib.qlora_layernorm_fwd(x[:1001])
+    dx = lib.qlora_layernorm_bwd(x, y, mean, rstd, need_dw=False, need_db=False)[0]
+    dx1 = lib.qlora_layernorm_bwd(x[:1001], y1, mean1, rstd1, need_dw=False, need_db=False)[0]
+    for got, one in ((y, y1), (mean, mean1), (rstd, rstd1), (dx, dx1)):
+        whole = m // 1001 * 1001
+        assert bool((got[:whole].view(-1, *one.shape) == one).all()) and torch.equal(got[whole:], one[:m - whole])
+    say("logprob 2^23 rows")
+    m, v = (1 << 23) + 9, 9
+    x = torch.randn(1001, v, device="cuda").bfloat16().repeat(m // 1001 + 1, 1)[:m].contiguous()
+    t = torch.arange(1001, device="cuda").repeat(m // 1001 + 1)[:m] % 10
+    out = lib.qlora_logprob_fwd(x, t, top=2)
+    one = lib.qlora_logprob_fwd(x[:1001], t[:1001], top=2)
+    g = torch.ones(m, device="cuda")
+    d = lib.qlora_logprob_bwd(x, t, out[2], out[1], g, g)
+    d1 = lib.qlora_logprob_bwd(x[:1001], t[:1001], one[2], one[1], g[:1001], g[:1001])
+    for got, want in (*zip(out, one), (d, d1)):
+        whole = m // 1001 * 1001
+        assert bool((got[:whole].view(-1, *want.shape) == want).all()) and torch.equal(got[whole:], want[:m - whole])
+
+
 def test_attention_past_2_31_elements(lib):
     """2^31 + elements of q and of each gradient; the sequences are short."""
     say("attention past 2^31 elements")

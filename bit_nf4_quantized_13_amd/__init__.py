@@ -480,7 +480,7 @@ def qlora_layernorm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bia
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _shaped(t, ref.dtype, (n,), name)
-    y = _shaped(out, x.dtype, (m, n), "out") if out is not None else torch.empty((m, n), dtype=x.dtype, device=x.device)
+    y = _shaped(out, x.dtype, (m, n), "out") if out is not None else torch.empty(m, n, dtype=x.dtype, device=x.device)
     mean = torch.empty(m, dtype=torch.float32, device=x.device) if save_stats else None
     rstd = torch.empty_like(mean) if save_stats else None
     _check(_lib.qlora_layernorm_fwd(x.data_ptr(), kind, m, n, ld, _ptr(weight), _ptr(bias), wkind, float(eps),
@@ -509,7 +509,7 @@ def qlora_layernorm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
             if t is not None:
                 _shaped(t, torch.float32, (n,), name)
     else:
-        dx = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(dy)
         dw = torch.empty(n, dtype=torch.float32, device=x.device) if need_dw else None
         db = torch.empty(n, dtype=torch.float32, device=x.device) if need_db else None
     ws = workspace
@@ -531,25 +531,29 @@ def _heads(t: torch.Tensor, rows: int, dim: int, name: str) -> int:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [{rows}, heads, {dim}], got {list(t.shape)}")
-    width = t.shape[1] * dim
-    if (dim > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != dim:
+        raise ValueError(f"{name} must have shape [{rows}, heads, {dim}], got {list(shape)}")
+    heads, (pitch, head_pitch, step) = shape[1], t.stride()
+    if (dim > 1 and step != 1) or (heads > 1 and head_pitch != dim):
         raise ValueError(f"{name} must have its heads side by side in dense rows")
-    if rows > 1 and t.stride(0) < width:
+    if rows < 2:
+        return heads * dim
+    if pitch < heads * dim:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0) if rows > 1 else width
+    return pitch
 
 
 def _attention_shape(q, k, v, cu_seqlens, scale) -> _CAttentionShape:
     if q.dim() != 3:
         raise ValueError("q must have shape [rows, heads, dim]")
     rows, heads, dim = q.shape
-    ldq, ldk, ldv = (_heads(t, rows, dim, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
-    if k.shape[1] != v.shape[1]:
+    ldq, ldk, ldv = _heads(q, rows, dim, "q"), _heads(k, rows, dim, "k"), _heads(v, rows, dim, "v")
+    kv_heads = k.shape[1]
+    if kv_heads != v.shape[1]:
         raise ValueError("k and v must have the same heads")
     _dev_tensor(cu_seqlens, torch.int32, "cu_seqlens")
-    return _CAttentionShape(rows, cu_seqlens.numel() - 1, heads, k.shape[1], dim, ldq, ldk, ldv,
+    return _CAttentionShape(rows, cu_seqlens.numel() - 1, heads, kv_heads, dim, ldq, ldk, ldv,
                             dim ** -0.5 if scale is None else scale)
 
 
@@ -560,10 +564,11 @@ def qlora_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     Returns (o like q, lse fp32 [heads, T], residual like o or None); the residual is what the backward
     takes to be exact in o.  scale: dim ** -0.5 if not given."""
     shape = _attention_shape(q, k, v, cu_seqlens, scale)
+    rows, heads, dim = q.shape
     o = _shaped(out, torch.bfloat16, q.shape, "out") if out is not None else torch.empty(
-        q.shape, dtype=torch.bfloat16, device=q.device)
-    res = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if save_residual else None
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        rows, heads, dim, dtype=torch.bfloat16, device=q.device)
+    res = torch.empty_like(o) if save_residual else None
+    lse = torch.empty(heads, rows, dtype=torch.float32, device=q.device)
     _check(_lib.qlora_attention_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                     cu_seqlens.data_ptr(), o.data_ptr(), _ptr(res), lse.data_ptr(), _stream()),
            "qlora_attention_fwd")
@@ -582,14 +587,20 @@ def qlora_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: to
     _shaped(lse, torch.float32, (q.shape[1], q.shape[0]), "lse")
     if residual is not None:
         _shaped(residual, torch.bfloat16, q.shape, "residual")
-    dq, dk, dv = outs if outs is not None else (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
-                                                for t in (q, k, v))
-    rows, _, dim = q.shape
-    pitches = []
-    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {list(like.shape)}")
-        pitches.append(_heads(t, rows, dim, name))
+    rows, heads, dim = q.shape
+    if outs is None:
+        kv_heads, device = k.shape[1], q.device
+        dq = torch.empty_like(o)
+        dk = torch.empty(rows, kv_heads, dim, dtype=torch.bfloat16, device=device)
+        dv = torch.empty_like(dk)
+        pitches = heads * dim, kv_heads * dim, kv_heads * dim
+    else:
+        dq, dk, dv = outs
+        pitches = []
+        for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must have shape {list(like.shape)}")
+            pitches.append(_heads(t, rows, dim, name))
     ws = workspace if workspace is not None else _workspace(
         int(_lib.qlora_attention_workspace(ctypes.byref(shape))), q.device)
     _check(_lib.qlora_attention_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
@@ -612,10 +623,11 @@ def qlora_logprob_fwd(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
     kind, ld = _element_type(logits, "logits"), _rows(logits, "logits")
     m, v = logits.shape
     _shaped(targets, torch.int64, (m,), "targets")
-    logp, entropy, lse = torch.empty((3, m), dtype=torch.float32, device=logits.device).unbind(0)
-    top_logp = torch.empty((m, top), dtype=torch.float32, device=logits.device) if top > 0 else None
-    top_ids = torch.empty((m, top), dtype=torch.int32, device=logits.device) if top > 0 else None
-    ws = workspace if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), logits.device)
+    device = logits.device
+    logp, entropy, lse = torch.empty(3, m, dtype=torch.float32, device=device).unbind(0)
+    top_logp = torch.empty(m, top, dtype=torch.float32, device=device) if top > 0 else None
+    top_ids = torch.empty_like(top_logp, dtype=torch.int32) if top > 0 else None
+    ws = workspace if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), device)
     _check(_lib.qlora_logprob_fwd(logits.data_ptr(), kind, m, v, ld, targets.data_ptr(), int(top), logp.data_ptr(),
                                   entropy.data_ptr(), lse.data_ptr(), _ptr(top_logp), _ptr(top_ids), ws.data_ptr(),
                                   ws.numel(), _stream()), "qlora_logprob_fwd")
@@ -634,7 +646,7 @@ def qlora_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Te
         if t is not None:
             _shaped(t, torch.float32, (m,), name)
     if out is None:
-        out = torch.empty((m, v), dtype=logits.dtype, device=logits.device)
+        out = torch.empty(m, v, dtype=logits.dtype, device=logits.device)
     elif out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' type and shape")
     _check(_lib.qlora_logprob_bwd(logits.data_ptr(), kind, m, v, ld, targets.data_ptr(), _ptr(lse), _ptr(entropy),

@@ -34,24 +34,21 @@
 // second factor of ds at once.  delta's o is taken with its rounding residual where the
 // forward saved it, so that the bf16 of o does not enter dS.
 //
-// A workgroup is 4 waves (or two parts of 4) with 32 rows each; the tiles of the other side
+// A workgroup is 4 waves (or 8, in parts) with 32 rows each; the tiles of the other side
 // are brought to LDS by direct transfers, one tile ahead.  Tile rows are 16-byte
 // chunks in an order that depends on the row, so that both the row reads (one
 // chunk of 16 rows) and the transposing reads (4 chunks of 4 rows) fall on all
 // banks.  Head dimensions are padded to 64 or 128 with zeros in LDS.
 //
 // Workgroups find their tile without a list: sequence s owns the slots from
-// start_s / 128 + s on, which is enough for its tiles whatever its start (128
-// rows a tile); a workgroup looks its slot up among the starts, 64 at a time.
+// start_s / OWN + s on, which is enough for its tiles whatever its start (OWN rows
+// a tile); a workgroup looks its slot up among the starts, 64 at a time.
 #include "launch.hpp"
 
 namespace qnf4 {
 namespace {
 
-constexpr int kWaves = 4;          // of a workgroup with one part
-constexpr int kThreads = 64 * kWaves;
-constexpr int kOwn = 32 * kWaves;  // rows a workgroup owns
-constexpr int kStream = 64;        // rows of a tile that passes through LDS
+constexpr int kThreads = 256;      // of the kernel that adds partials
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -113,6 +110,7 @@ __device__ __forceinline__ int bound_at(const int32_t *cu, int S, int T, int i) 
     const int c = cu[i - 1];
     return c < 0 ? 0 : c > T ? T : c;
 }
+template <int OWN>
 __device__ __forceinline__ Place place_of(const int32_t *cu, int S, int T, int slot) {
     const int lane = threadIdx.x & 63;
     int lo = 0, len = S + 2, n, bound, step;
@@ -120,7 +118,7 @@ __device__ __forceinline__ Place place_of(const int32_t *cu, int S, int T, int s
         step = (len + 63) / 64;
         const int i = lo + lane * step;
         bound = bound_at(cu, S, T, i);
-        n = __popcll(__ballot(lane * step < len && bound / kOwn + i <= slot));
+        n = __popcll(__ballot(lane * step < len && bound / OWN + i <= slot));
         n = __builtin_amdgcn_readfirstlane(n < 1 ? 1 : n);
         const int left = len - (n - 1) * step;
         lo += (n - 1) * step;
@@ -129,7 +127,7 @@ __device__ __forceinline__ Place place_of(const int32_t *cu, int S, int T, int s
     Place p;  // the last step's lanes hold the segments' starts one by one
     p.begin = __builtin_amdgcn_readlane(bound, n - 1);
     p.end = n < 64 ? __builtin_amdgcn_readlane(bound, n) : __builtin_amdgcn_readfirstlane(bound_at(cu, S, T, lo + 1));
-    p.first = p.begin + (slot - (p.begin / kOwn + lo)) * kOwn;
+    p.first = p.begin + (slot - (p.begin / OWN + lo)) * OWN;
     p.outside = lo == 0 || lo == S + 1;
     return p;
 }
@@ -292,9 +290,10 @@ __device__ __forceinline__ void store_rows(void *lds, uint16_t *y, uint16_t *res
 }
 
 // Zeros in the rows [row0, end) of one head, by the whole workgroup.
+template <int OWN>
 __device__ __forceinline__ void zero_rows(uint16_t *y, int64_t ld, int row0, int end, int D) {
     const int chunks = D / 8;
-    for (int i = threadIdx.x; i < kOwn * chunks; i += blockDim.x) {
+    for (int i = threadIdx.x; i < OWN * chunks; i += blockDim.x) {
         const int row = row0 + i / chunks;
         if (row < end) *reinterpret_cast<uint4 *>(y + (int64_t)row * ld + (i % chunks) * 8) = make_uint4(0, 0, 0, 0);
     }
@@ -304,9 +303,24 @@ __device__ __forceinline__ void zero_rows(uint16_t *y, int64_t ld, int row0, int
 // heads, so that the heads of a group and the tiles of a head meet in one L2.
 __device__ __forceinline__ int head_of(int p, int H, int Hk) { return (p % Hk) * (H / Hk) + p / Hk; }
 
-// Where there are few workgroups, PARTS = 2 groups of 4 waves share a workgroup's rows,
-// each with its own rows of every tile, and their results meet in LDS at the end: a
-// lane's registers, 64 apart.
+// A workgroup's waves: GROUPS of 32 rows, each group in PARTS.  Where there are few
+// workgroups, the parts share their group's rows, each with its own rows of every tile,
+// and their results meet in LDS at the end: a lane's registers, 64 apart.
+template <int DP, int PARTS, int GROUPS>
+struct Team {
+    static constexpr int kFloats = DP / 2 * 64;  // of a wave's accumulators
+    int lane, wave, group, part;
+    __device__ __forceinline__ Team() {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        group = wave % GROUPS;
+        part = wave / GROUPS;
+    }
+    // Where a part's results wait for the one that adds them: slot 0 .. PARTS - 2.
+    __device__ __forceinline__ float *slot(void *lds, int i) const {
+        return static_cast<float *>(lds) + (i * GROUPS + group) * kFloats;
+    }
+};
 template <int N>
 __device__ __forceinline__ void put_tiles(float *to, const f32x16 *t) {
 #pragma unroll
@@ -322,37 +336,36 @@ __device__ __forceinline__ void add_tiles(f32x16 *t, float f, const float *from,
         for (int i = 0; i < 16; ++i) t[dt][i] = t[dt][i] * f + from[(dt * 16 + i) * 64] * g;
 }
 
-template <int DP, int PARTS>
-__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
+template <int DP, int PARTS, int GROUPS>
+__global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(AttentionShape a, const uint16_t *__restrict__ q,
                                                                  const uint16_t *__restrict__ k,
                                                                  const uint16_t *__restrict__ v,
                                                                  const int32_t *__restrict__ cu,
                                                                  uint16_t *__restrict__ o, uint16_t *__restrict__ res,
                                                                  float *__restrict__ lse, int slots) {
-    constexpr int kStep = kStream * PARTS;
+    constexpr int OWN = 32 * GROUPS, kShare = GROUPS == 4 ? 64 : 32, kStep = kShare * PARTS;  // rows of a tile: a part's, all
     __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStep * DP];
     uint16_t(*ks_)[kStep * DP] = tiles_, (*vs_)[kStep * DP] = tiles_ + 2;
-    __shared__ float meet[2][PARTS > 1 ? kThreads : 1];
+    __shared__ float meet[2][PARTS > 1 ? 64 * PARTS * GROUPS : 1];
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     // the long rows' tiles first
-    const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
+    const Place at = place_of<OWN>(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
     const int64_t ldo = (int64_t)a.H * a.D;
-    const int last = at.first + kOwn < at.end ? at.first + kOwn : at.end;
+    const int last = at.first + OWN < at.end ? at.first + OWN : at.end;
     if (at.outside) {
-        zero_rows(o + head * a.D, ldo, at.first, last, a.D);
-        if (res) zero_rows(res + head * a.D, ldo, at.first, last, a.D);
-        for (int i = at.first + threadIdx.x; i < last; i += kThreads * PARTS) lse[(int64_t)head * a.T + i] = -INFINITY;
+        zero_rows<OWN>(o + head * a.D, ldo, at.first, last, a.D);
+        if (res) zero_rows<OWN>(res + head * a.D, ldo, at.first, last, a.D);
+        for (int i = at.first + threadIdx.x; i < last; i += blockDim.x) lse[(int64_t)head * a.T + i] = -INFINITY;
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
-    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
-    const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP, kStep, kWaves * PARTS, true> mk, mv;
+    const Team<DP, PARTS, GROUPS> team;
+    const int l = team.lane, h = l >> 5, part = team.part, row0 = at.first + 32 * team.group, row = row0 + (l & 31);
+    Mover<DP, kStep, PARTS * GROUPS, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
     Reader<DP, true> rd;
-    rd.init(kStream * part);
+    rd.init(kShare * part);
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     bf16x8 qf[DP / 16];
     load_rows<DP>(q + (int64_t)head * a.D, a.ldq, row0, at.end, a.D, qf);
@@ -370,31 +383,31 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(Atte
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
         __syncthreads();  // tile j is in LDS, and nobody reads the other buffer
-        const int tile0 = at.begin + j * kStep, key0 = tile0 + kStream * part;
+        const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
         if (j + 1 < tiles) {
             mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
             mv.load(vh, a.ldv, a.D, tile0 + kStep, at.end, lds_addr(vs_[1 - B]));
         }
         if (key0 > row0 + 31) return;  // the wave's rows all come before this tile
         const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
-        f32x16 s[2];
+        f32x16 s[kShare / 32];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kShare / 32; ++t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) s[t] = mfma(rd.rows(kt_, t, ks), qf[ks], s[t]);
         }
-        if (key0 + kStream - 1 > row0) {
+        if (key0 + kShare - 1 > row0) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < kShare / 32; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (key0 + 32 * t + tile_row(i) > row - 4 * h) s[t][i] = -INFINITY;
         }
         float top = s[0][0];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kShare / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         top = pair_max(top);
@@ -413,14 +426,14 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(Atte
         }
         const float mc = PARTS > 1 && m == -INFINITY ? 0.0f : m * c;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kShare / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -mc));
                 sum += s[t][i];
             }
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
+        for (int st = 0; st < kShare / 16; ++st) {
             const bf16x8 p = operand_of(s[st >> 1], st & 1);
 #pragma unroll
             for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(vt_, dt, st), p, acc[dt]);
@@ -431,55 +444,56 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_fwd_kernel(Atte
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     sum = pair_sum(sum);
-    float *mine = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64;
+    float *mine = team.slot(tiles_, 0);
     __syncthreads();  // the tiles are read
     if (PARTS > 1) {
-        float *other = mine + l;
-        if (part == 1) {
-            put_tiles<DP / 32>(other, acc);
-            meet[0][wave * 64 + l] = m;
-            meet[1][wave * 64 + l] = sum;
-        }
+        if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
+        meet[0][threadIdx.x] = m;
+        meet[1][threadIdx.x] = sum;
         __syncthreads();
-        if (part == 1) return;
-        const float m1 = meet[0][wave * 64 + l], top = fmaxf(m, m1);
-        const float f0 = __builtin_amdgcn_exp2f((m - top) * c), f1 = __builtin_amdgcn_exp2f((m1 - top) * c);
-        add_tiles<DP / 32>(acc, f0, other, f1);
-        sum = sum * f0 + meet[1][wave * 64 + l] * f1;
-        m = top;
+        if (part > 0) return;
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) {
+            const int other = threadIdx.x + 64 * GROUPS * p;
+            const float m1 = meet[0][other], top = fmaxf(m, m1);  // the first part has met the first key: not -inf
+            const float f0 = __builtin_amdgcn_exp2f((m - top) * c), f1 = __builtin_amdgcn_exp2f((m1 - top) * c);
+            add_tiles<DP / 32>(acc, f0, team.slot(tiles_, p - 1) + l, f1);
+            sum = sum * f0 + meet[1][other] * f1;
+            m = top;
+        }
     }
     store_rows<DP>(mine, o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
     if (h == 0 && row < at.end) lse[(int64_t)head * a.T + row] = m * a.scale + logf(sum);
 }
 
 // dq, and the rows' statistics for the dk, dv kernel.
-template <int DP, int PARTS>
-__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
+template <int DP, int PARTS, int GROUPS>
+__global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
     const uint16_t *__restrict__ o, const uint16_t *__restrict__ res, const float *__restrict__ lse,
     const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, uint16_t *__restrict__ dq, int64_t lddq,
     float *__restrict__ stats, int slots) {
-    __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStream * DP];
-    uint16_t(*ks_)[kStream * DP] = tiles_, (*vs_)[kStream * DP] = tiles_ + 2;
+    constexpr int OWN = 32 * GROUPS, kShare = PARTS == 1 ? 64 : 32, kStep = kShare * PARTS;
+    __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStep * DP];
+    uint16_t(*ks_)[kStep * DP] = tiles_, (*vs_)[kStep * DP] = tiles_ + 2;
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
-    const Place at = place_of(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
+    const Place at = place_of<OWN>(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
     const int64_t ldo = (int64_t)a.H * a.D;
-    const int last = at.first + kOwn < at.end ? at.first + kOwn : at.end;
+    const int last = at.first + OWN < at.end ? at.first + OWN : at.end;
     if (at.outside) {
-        zero_rows(dq + head * a.D, lddq, at.first, last, a.D);
+        zero_rows<OWN>(dq + head * a.D, lddq, at.first, last, a.D);
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
-    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
-    const int row0 = at.first + 32 * wave, row = row0 + (l & 31);
-    Mover<DP, kStream, kWaves * PARTS, true> mk, mv;
+    const Team<DP, PARTS, GROUPS> team;
+    const int l = team.lane, h = l >> 5, part = team.part, row0 = at.first + 32 * team.group, row = row0 + (l & 31);
+    Mover<DP, kStep, PARTS * GROUPS, true> mk, mv;
     mk.init(a.ldk, a.D);
     mv.init(a.ldv, a.D);
     Reader<DP, true> rd;
-    rd.init(32 * part);
+    rd.init(kShare * part);
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
-    const int tiles = (last - at.begin + kStream - 1) / kStream;
+    const int tiles = (last - at.begin + kStep - 1) / kStep;
     mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
     mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
     bf16x8 qf[DP / 16], df[DP / 16];
@@ -517,15 +531,15 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
         __syncthreads();
-        const int key0 = at.begin + j * kStream;
+        const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
         if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, a.D, key0 + kStream, at.end, lds_addr(ks_[1 - B]));
-            mv.load(vh, a.ldv, a.D, key0 + kStream, at.end, lds_addr(vs_[1 - B]));
+            mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
+            mv.load(vh, a.ldv, a.D, tile0 + kStep, at.end, lds_addr(vs_[1 - B]));
         }
         const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
 #pragma unroll
-        for (int t = 0; t < 2 / PARTS; ++t) {
-            const int k0 = key0 + 32 * (t + part);
+        for (int t = 0; t < kShare / 32; ++t) {
+            const int k0 = key0 + 32 * t;
             if (k0 > row0 + 31) break;
             f32x16 s, dp;
 #pragma unroll
@@ -557,14 +571,14 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dq_kernel(
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
-    float *mine = reinterpret_cast<float *>(tiles_) + wave * (DP / 2) * 64;
+    float *mine = team.slot(tiles_, 0);
     __syncthreads();  // the tiles are read
     if (PARTS > 1) {
-        float *other = mine + l;
-        if (part == 1) put_tiles<DP / 32>(other, acc);
+        if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
         __syncthreads();
-        if (part == 1) return;
-        add_tiles<DP / 32>(acc, 1.0f, other, 1.0f);
+        if (part > 0) return;
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) add_tiles<DP / 32>(acc, 1.0f, team.slot(tiles_, p - 1) + l, 1.0f);
     }
     store_rows<DP>(mine, dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
 }
@@ -597,40 +611,38 @@ __device__ __forceinline__ void store_rows_f32(float *y, int64_t ld, int row0, i
 // head, partial results) or of all heads of the group.  The keys stay in LDS and
 // the values in registers: with both in registers the two accumulators leave no
 // room for two waves a SIMD.
-template <int DP, bool SPLIT, int PARTS>
-__global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
+template <int DP, bool SPLIT, int PARTS, int GROUPS>
+__global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
     AttentionShape a, const uint16_t *__restrict__ q, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
     const float *__restrict__ stats, const uint16_t *__restrict__ dout, const int32_t *__restrict__ cu, KvOut out) {
-    constexpr int kTile = 32 * PARTS;
-    // the keys and the tiles; at the end of two parts dk and dv on their way from one to the other
-    constexpr int kLds = PARTS > 1 ? 4 * kOwn * DP : kOwn * DP + 4 * kTile * DP;
-    __shared__ __attribute__((aligned(256))) uint16_t lds_[kLds];
+    constexpr int OWN = 32 * GROUPS, kTile = 32 * PARTS;
+    __shared__ __attribute__((aligned(256))) uint16_t lds_[(OWN + 4 * kTile) * DP];
     uint16_t *ks_ = lds_;
-    uint16_t(*qs_)[kTile * DP] = reinterpret_cast<uint16_t(*)[kTile * DP]>(lds_ + kOwn * DP), (*ds_)[kTile * DP] = qs_ + 2;
+    uint16_t(*qs_)[kTile * DP] = reinterpret_cast<uint16_t(*)[kTile * DP]>(lds_ + OWN * DP), (*ds_)[kTile * DP] = qs_ + 2;
+    static_assert(PARTS == 1 || (PARTS - 1) * GROUPS * DP / 2 * 64 * 4 <= sizeof(lds_), "the parts' results");
     __shared__ __attribute__((aligned(16))) float ls_[2][kTile], dl_[2][kTile];
     const int group = a.H / a.Hk, heads = SPLIT ? a.H : a.Hk;
     const int first_head = SPLIT ? head_of(blockIdx.x % a.H, a.H, a.Hk) : (int)(blockIdx.x % a.Hk) * group;
     const int kv = first_head / group;
-    const Place at = place_of(cu, a.S, a.T, (int)(blockIdx.x / heads));  // the first keys have the most rows
+    const Place at = place_of<OWN>(cu, a.S, a.T, (int)(blockIdx.x / heads));  // the first keys have the most rows
     if (at.first >= at.end) return;
     const int64_t ldo = (int64_t)a.H * a.D;
     float *pk = SPLIT ? out.part + (int64_t)first_head * a.T * a.D : nullptr;
     float *pv = SPLIT ? out.part + ((int64_t)a.H + first_head) * a.T * a.D : nullptr;
     if (at.outside) {
-        const int last = at.first + kOwn < at.end ? at.first + kOwn : at.end;
+        const int last = at.first + OWN < at.end ? at.first + OWN : at.end;
         if (SPLIT) {
-            zero_rows(reinterpret_cast<uint16_t *>(pk), 2 * a.D, at.first, last, 2 * a.D);
-            zero_rows(reinterpret_cast<uint16_t *>(pv), 2 * a.D, at.first, last, 2 * a.D);
+            zero_rows<OWN>(reinterpret_cast<uint16_t *>(pk), 2 * a.D, at.first, last, 2 * a.D);
+            zero_rows<OWN>(reinterpret_cast<uint16_t *>(pv), 2 * a.D, at.first, last, 2 * a.D);
         } else {
-            zero_rows(out.dk + kv * a.D, out.lddk, at.first, last, a.D);
-            zero_rows(out.dv + kv * a.D, out.lddv, at.first, last, a.D);
+            zero_rows<OWN>(out.dk + kv * a.D, out.lddk, at.first, last, a.D);
+            zero_rows<OWN>(out.dv + kv * a.D, out.lddv, at.first, last, a.D);
         }
         return;
     }
-    const int l = threadIdx.x & 63, h = l >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
-    const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
-    const int key0 = at.first + 32 * wave, key = key0 + (l & 31);
-    Mover<DP, kTile, kWaves * PARTS, true> mq, md;
+    const Team<DP, PARTS, GROUPS> team;
+    const int l = team.lane, h = l >> 5, part = team.part, key0 = at.first + 32 * team.group, key = key0 + (l & 31);
+    Mover<DP, kTile, PARTS * GROUPS, true> mq, md;
     mq.init(a.ldq, a.D);
     md.init(ldo, a.D);
     Reader<DP, true> rd;
@@ -640,14 +652,17 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
     auto fetch = [&](int hd, int r0, int b) {
         mq.load(q + (int64_t)hd * a.D, a.ldq, a.D, r0, at.end, lds_addr(qs_[b]));
         md.load(dout + (int64_t)hd * a.D, ldo, a.D, r0, at.end, lds_addr(ds_[b]));
-        if (part == 0 && wave < 2 && l < kTile) {
-            const __amdgpu_buffer_rsrc_t r = out_rsrc(stats + (int64_t)(wave * a.H + hd) * a.T + r0, (int64_t)(at.end - r0) * 4);
-            transfer4(r, lds_addr(wave ? dl_[b] : ls_[b]), l * 4);
+        constexpr int kPieces = (kTile + 63) / 64;  // of 64 statistics
+        if (team.wave < 2 * kPieces && l < kTile) {
+            const int which = team.wave & 1, from = (team.wave >> 1) * 64;
+            const __amdgpu_buffer_rsrc_t r =
+                out_rsrc(stats + (int64_t)(which * a.H + hd) * a.T + r0, (int64_t)(at.end - r0) * 4);
+            transfer4(r, lds_addr((which ? dl_[b] : ls_[b]) + from), (from + l) * 4);
         }
     };
     int hd = first_head, r0 = at.first;  // of the tile at hand
     {
-        Mover<DP, kOwn, kWaves * PARTS, false> mk;
+        Mover<DP, OWN, PARTS * GROUPS, false> mk;
         mk.init(a.ldk, a.D);
         mk.load(k + (int64_t)kv * a.D, a.ldk, a.D, at.first, at.end, lds_addr(ks_));
     }
@@ -660,7 +675,7 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.0f;
     const float c = a.scale * kLog2e;
-    uint32_t kt_ = lds_addr(ks_) + 32 * (wave - part) * DP * 2;  // the reader is 32 part rows ahead
+    uint32_t kt_ = lds_addr(ks_) + 32 * (team.group - part) * DP * 2;  // the reader is 32 part rows ahead
     const int per = (at.end - at.first + kTile - 1) / kTile, tiles = per * (SPLIT ? 1 : group);
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
@@ -720,23 +735,29 @@ __global__ __launch_bounds__(kThreads * PARTS, 2) void attention_dkv_kernel(
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
-    float *mine = reinterpret_cast<float *>(lds_) + (part * kWaves + wave) * (DP / 2) * 64;
+    // dk is the first part's to add and store, dv the second's, one after the other
+    float *mine = team.slot(lds_, 0);
     __syncthreads();  // the tiles are read
     if (PARTS > 1) {
-        float *dk = reinterpret_cast<float *>(lds_) + wave * (DP / 2) * 64 + l, *dv = dk + kWaves * (DP / 2) * 64;
-        if (part == 1) put_tiles<DP / 32>(dk, ak);
-        else put_tiles<DP / 32>(dv, av);
+        if (part > 0) put_tiles<DP / 32>(team.slot(lds_, part - 1) + l, ak);
         __syncthreads();
-        if (part == 0) add_tiles<DP / 32>(ak, 1.0f, dk, 1.0f);
-        else add_tiles<DP / 32>(av, 1.0f, dv, 1.0f);
     }
-    const bool has_k = part == 0, has_v = part == PARTS - 1;
-    if (SPLIT) {
-        if (has_k) store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
-        if (has_v) store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
-    } else {
-        if (has_k) store_rows<DP>(mine, out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
-        if (has_v) store_rows<DP>(mine, out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
+    if (part == 0) {
+#pragma unroll 1
+        for (int p = 1; p < PARTS; ++p) add_tiles<DP / 32>(ak, 1.0f, team.slot(lds_, p - 1) + l, 1.0f);
+        if (SPLIT) store_rows_f32<DP>(pk, a.D, key0, at.end, a.D, ak, a.scale);
+        else store_rows<DP>(mine, out.dk + kv * a.D, nullptr, out.lddk, key0, at.end, a.D, ak, a.scale);
+    }
+    if (PARTS > 1) {
+        __syncthreads();
+        if (part != 1) put_tiles<DP / 32>(team.slot(lds_, part > 1 ? part - 1 : 0) + l, av);
+        __syncthreads();
+    }
+    if (part == (PARTS > 1 ? 1 : 0)) {
+#pragma unroll 1
+        for (int p = 1; p < PARTS; ++p) add_tiles<DP / 32>(av, 1.0f, team.slot(lds_, p - 1) + l, 1.0f);
+        if (SPLIT) store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
+        else store_rows<DP>(mine, out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
     }
 }
 
@@ -758,7 +779,8 @@ __global__ __launch_bounds__(kThreads) void attention_group_sum_kernel(Attention
                                                pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
 }
 
-int slots_of(const AttentionShape &a) { return a.T / kOwn + a.S + 2; }
+// Slots of a head for workgroups of `own` rows.
+int slots_of(const AttentionShape &a, int own) { return a.T / own + a.S + 2; }
 
 // A workgroup a head instead of a group in the dk, dv kernel.  With a group a
 // workgroup, the first keys of a sequence of L rows take group L / 32 steps, and the
@@ -773,31 +795,37 @@ bool split_heads(const AttentionShape &a) {
     return a.H > a.Hk && len * 131072 > (double)a.T * a.Hk * (len + 1536);
 }
 
-// Two parts where the workgroups (about T H / 128) are no more than the 512 that run
-// at a time with one part, and sequences long enough for the steps saved to pay for
-// the parts' meeting.  Backward, one part / two (us): 1 x 8192 H / Hk 8 / 2 D 128 638 / 491, 2 x 2048 16 / 16 D 64
+// Parts, from the mean length L of the sequences and the T H rows of all heads.  Two
+// where the workgroups (about T H / 128) are no more than the 512 that run at a time
+// with one part, and sequences long enough for the steps saved to pay for the parts'
+// meeting.  Backward, one part / two (us): 1 x 8192 H / Hk 8 / 2 D 128 638 / 491, 2 x 2048 16 / 16 D 64
 // 131 / 97, 1 x 500 32 / 32 D 128 51 / 47; 2 x 256 8 / 8 D 128 33 / 34, 4 x 512 32 / 32 D 64 49 / 56,
 // 1 x 8192 16 / 4 D 128 939 / 966.  Forward, the same: 174 / 154, 43 / 40, 17 / 17; 11 / 13, 18 / 19, 289 / 301.
-bool two_parts(const AttentionShape &a) {
+// Four, with 64 rows a workgroup instead of 128, where the workgroups leave CUs idle.  Forward +
+// backward, two / four: 1 x 4096 4 / 4 D 128 242 / 161, 1 x 2048 8 / 8 D 64 87 / 59, (900, 60, 30) 8 / 8
+// D 80 85 / 59, 1 x 4096 8 / 2 D 128 260 / 222; 2 x 1024 16 / 16 D 128 89 / 102, 2 x 2048 16 / 16 D 64 127 / 145.
+int parts_of(const AttentionShape &a) {
     const int64_t len = a.T / a.S, rows = (int64_t)a.T * a.H;
-    return len >= 384 && rows <= 65536 && rows <= 80 * len;
+    if (len >= 300 && rows <= 32768 && rows <= 24 * len) return 4;
+    return len >= 384 && rows <= 65536 && rows <= 80 * len ? 2 : 1;
 }
 size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
 
-template <int DP, int PARTS>
+template <int DP, int PARTS, int GROUPS>
 hipError_t backward(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                     const uint16_t *o, const uint16_t *res, const float *lse, const uint16_t *dout, const int32_t *cu,
                     uint16_t *dq, int64_t lddq, float *stats, const KvOut &out, hipStream_t s) {
-    constexpr int kT = kThreads * PARTS;
-    const int slots = slots_of(a);
-    attention_dq_kernel<DP, PARTS><<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, slots);
+    constexpr int kT = 64 * PARTS * GROUPS;
+    const int slots = slots_of(a, 32 * GROUPS);
+    attention_dq_kernel<DP, PARTS, GROUPS>
+        <<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, slots);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!split_heads(a)) {
-        attention_dkv_kernel<DP, false, PARTS><<<(unsigned)slots * a.Hk, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+        attention_dkv_kernel<DP, false, PARTS, GROUPS><<<(unsigned)slots * a.Hk, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
         return hipGetLastError();
     }
-    attention_dkv_kernel<DP, true, PARTS><<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
+    attention_dkv_kernel<DP, true, PARTS, GROUPS><<<(unsigned)slots * a.H, kT, 0, s>>>(a, q, k, v, stats, dout, cu, out);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t chunks = (int64_t)a.T * a.Hk * (a.D / 8);
@@ -805,20 +833,22 @@ hipError_t backward(const AttentionShape &a, const uint16_t *q, const uint16_t *
     return hipGetLastError();
 }
 
-// f with the padded head dimension and the parts as template values.
+// f with the padded head dimension, the parts and the groups as template values.
 template <typename F>
 hipError_t shaped(const AttentionShape &a, F f) {
-    using std::integral_constant;
-    if (a.D <= 64)
-        return two_parts(a) ? f(integral_constant<int, 64>(), integral_constant<int, 2>())
-                            : f(integral_constant<int, 64>(), integral_constant<int, 1>());
-    return two_parts(a) ? f(integral_constant<int, 128>(), integral_constant<int, 2>())
-                        : f(integral_constant<int, 128>(), integral_constant<int, 1>());
+    auto with = [&](auto dp) {
+        switch (parts_of(a)) {
+            case 4: return f(dp, std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+            case 2: return f(dp, std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+            default: return f(dp, std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
+        }
+    };
+    return a.D <= 64 ? with(std::integral_constant<int, 64>()) : with(std::integral_constant<int, 128>());
 }
 
 }  // namespace
 
-int64_t attention_groups(const AttentionShape &a) { return (int64_t)slots_of(a) * a.H; }
+int64_t attention_groups(const AttentionShape &a) { return (int64_t)slots_of(a, 64) * a.H; }
 
 size_t attention_bwd_bytes(const AttentionShape &a) {
     return stats_bytes(a) + (split_heads(a) ? sizeof(float) * 2 * (size_t)a.T * a.H * a.D : 0);
@@ -826,10 +856,11 @@ size_t attention_bwd_bytes(const AttentionShape &a) {
 
 hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s) {
-    const int slots = slots_of(a);
-    return shaped(a, [&](auto dp, auto parts) {
-        constexpr int kDp = decltype(dp)::value, kParts = decltype(parts)::value;
-        attention_fwd_kernel<kDp, kParts><<<(unsigned)slots * a.H, kThreads * kParts, 0, s>>>(a, q, k, v, cu, o, res, lse, slots);
+    return shaped(a, [&](auto dp, auto parts, auto groups) {
+        constexpr int kDp = decltype(dp)::value, kParts = decltype(parts)::value, kGroups = decltype(groups)::value;
+        const int slots = slots_of(a, 32 * kGroups);
+        attention_fwd_kernel<kDp, kParts, kGroups>
+            <<<(unsigned)slots * a.H, 64 * kParts * kGroups, 0, s>>>(a, q, k, v, cu, o, res, lse, slots);
         return hipGetLastError();
     });
 }
@@ -840,8 +871,8 @@ hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, cons
                                 uint16_t *dv, int64_t lddv, void *ws, hipStream_t s) {
     float *stats = static_cast<float *>(ws);
     const KvOut out{dk, dv, lddk, lddv, reinterpret_cast<float *>(static_cast<char *>(ws) + stats_bytes(a))};
-    return shaped(a, [&](auto dp, auto parts) {
-        return backward<decltype(dp)::value, decltype(parts)::value>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
+    return shaped(a, [&](auto dp, auto parts, auto groups) {
+        return backward<decltype(dp)::value, decltype(parts)::value, decltype(groups)::value>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
     });
 }
 

@@ -12,9 +12,10 @@
 // Bound: the matrix cores from a few hundred rows on (4 D operations a pair and
 // head forward, 14 D backward: s and dp are formed twice so that every sum has
 // one owner and a fixed order, no atomics), HBM below.  Measured at D = 128: one
-// sequence of 8192 rows, H / Hk = 32 / 8, forward 510 us (1.08 PFLOP/s; the matrix cores busy
-// 47 % of the time, the exponentials and conversions between the products beside
-// them); 4 x 1024, 32 / 32, forward 63 us, dq 87, dk and dv 105 (0.55 to 0.7 PFLOP/s).
+// sequence of 8192 rows, H / Hk = 32 / 8, forward 517 us (1.06 PFLOP/s; the matrix cores busy
+// 55 % of the time, the exponentials and conversions between the products and the
+// LDS reads beside them); 4 x 1024, 32 / 32, forward 57 to 68 us, dq 80 to 93, dk and dv
+// 88 to 105 (0.55 to 0.8 PFLOP/s).
 //
 // All products are 32 x 32 x 16 with the score tile transposed so that its
 // result layout is the next product's operand: the lane that receives score
@@ -50,7 +51,6 @@ namespace {
 
 constexpr int kThreads = 256;      // of the kernel that adds partials
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -240,7 +240,7 @@ __device__ __forceinline__ void load_rows(const uint16_t *x, int64_t ld, int row
 // way to memory: a lane holds 4 values of a row here and there, so the tile goes
 // through the wave's own LDS (32 rows of DP bf16, chunks of 16 bytes in an order that
 // depends on the row) and leaves as whole rows (8-byte pieces from the registers cost the
-// forward of 4 x 1024, 32 heads, OLD us against NEW).
+// forward of 4 x 1024, 32 heads, 69 us against 63).
 template <int DP>
 struct RowWriter {
     static constexpr int kChunks = DP / 8, kRows = 64 / kChunks;

@@ -795,19 +795,20 @@ bool split_heads(const AttentionShape &a) {
     return a.H > a.Hk && len * 131072 > (double)a.T * a.Hk * (len + 1536);
 }
 
-// Parts, from the mean length L of the sequences and the T H rows of all heads.  Two
-// where the workgroups (about T H / 128) are no more than the 512 that run at a time
-// with one part, and sequences long enough for the steps saved to pay for the parts'
-// meeting.  Backward, one part / two (us): 1 x 8192 H / Hk 8 / 2 D 128 638 / 491, 2 x 2048 16 / 16 D 64
-// 131 / 97, 1 x 500 32 / 32 D 128 51 / 47; 2 x 256 8 / 8 D 128 33 / 34, 4 x 512 32 / 32 D 64 49 / 56,
-// 1 x 8192 16 / 4 D 128 939 / 966.  Forward, the same: 174 / 154, 43 / 40, 17 / 17; 11 / 13, 18 / 19, 289 / 301.
-// Four, with 64 rows a workgroup instead of 128, where the workgroups leave CUs idle.  Forward +
-// backward, two / four: 1 x 4096 4 / 4 D 128 242 / 161, 1 x 2048 8 / 8 D 64 87 / 59, (900, 60, 30) 8 / 8
-// D 80 85 / 59, 1 x 4096 8 / 2 D 128 260 / 222; 2 x 1024 16 / 16 D 128 89 / 102, 2 x 2048 16 / 16 D 64 127 / 145.
+// Parts, from the mean length L of the sequences (the lengths themselves are on the
+// device) and the T H rows of all heads.  Four, with 64 rows a workgroup instead of 128,
+// where these run in one round (their LDS leaves one a CU for D > 64, two below), or
+// one long sequence is most of it.  Forward + backward, one part / two / four (us): 1 x 1024 H / Hk 8 / 8 D 128
+// 109 / 83 / 64, 2 x 512 16 / 16 D 128 59 / 58 / 51, (1000, 20, 20, 20, 20) 8 / 4 D 64 69 / 58 / 43, 4 x 256 8 / 8
+// D 128 40 / 43 / 41; beyond: 3 x 512 16 / 16 D 128 63 / 61 / 83, 8 x 128 16 / 4 D 128 45 / 51 / 52.
+// Two, of 128 rows, where the workgroups are no more than the 512 that run at a time
+// with one part: 1 x 8192 8 / 2 D 128 812 / 645, 2 x 2048 16 / 16 D 64 174 / 137, (2570, 37, 34, 0, 110, 2, 14, 5)
+// 8 / 8 D 128 204 / 169; beyond: 4 x 512 32 / 32 D 64 67 / 75, 1 x 8192 16 / 4 D 128 1228 / 1267.
 int parts_of(const AttentionShape &a) {
     const int64_t len = a.T / a.S, rows = (int64_t)a.T * a.H;
-    if (len >= 300 && rows <= 32768 && rows <= 24 * len) return 4;
-    return len >= 384 && rows <= 65536 && rows <= 80 * len ? 2 : 1;
+    const bool one_round = rows <= (a.D <= 64 ? 32768 : 16384), one_long = rows <= 32768 && rows <= 12 * len;
+    if (len >= 200 && (one_round || one_long)) return 4;
+    return len >= 300 && rows <= 65536 && rows <= 80 * len ? 2 : 1;
 }
 size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
 

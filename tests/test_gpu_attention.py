@@ -128,7 +128,7 @@ def test_packed_sequences(d):
 @pytest.mark.parametrize("lens,h,hk,d", [
     ([384], 2, 2, 64), ([385], 2, 1, 128), ([449, 703], 2, 2, 128), ([512, 1, 1040], 3, 1, 64), ([1027, 130, 0, 545], 4, 2, 72),
     ([800], 1, 1, 40), ([480, 480], 2, 2, 112), ([430, 450], 14, 7, 64), ([700], 28, 28, 128), ([600, 1, 3], 2, 1, 64),
-    ([3, 640, 1], 2, 2, 128)])
+    ([3, 640, 1], 2, 2, 128), ([600, 1, 3, 2, 0], 2, 1, 64), ([3, 640, 1, 1], 2, 2, 128), ([620, 0, 1300], 28, 7, 64)])
 def test_few_long_sequences(lens, h, hk, d):
     """Sequences whose rows one, two or four parts of a workgroup share."""
     check(lens, 7, h, hk, d, len(lens), fused=True, head=5)

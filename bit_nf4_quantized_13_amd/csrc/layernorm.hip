@@ -42,13 +42,25 @@ constexpr int kMaxRowGroups = 512;
 constexpr int64_t kLaunchRows = 1 << 21;  // of a launch with a workgroup a row: its threads stay below 2^32
 constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
 
-// Sum of v over the TPR threads of a row group (TPR a multiple of 64); every
+// Sum of v over the 16 lanes of a row group, or over the wave, on every lane: 16
+// lanes by rotations within them.
+template <int TPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if (TPR != 16) return wave_sum(v);
+    v += dpp_or<0x128, 0xF>(v, v);
+    v += dpp_or<0x124, 0xF>(v, v);
+    v += dpp_or<0x122, 0xF>(v, v);
+    v += dpp_or<0x121, 0xF>(v, v);
+    return v;
+}
+
+// Sum of v over the TPR threads of a row group (16, or a multiple of 64); every
 // thread of the workgroup calls it.  red: one float for each wave, not written
 // again before another barrier.
 template <int TPR>
 __device__ __forceinline__ float group_sum(float v, float *red) {
-    v = wave_sum(v);
-    if (TPR == 64) return v;
+    v = lanes_sum<TPR>(v);
+    if (TPR <= 64) return v;
     const int wave = threadIdx.x >> 6, w0 = threadIdx.x / TPR * (TPR / 64);
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
@@ -197,8 +209,8 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
         }
         // the rows of the next pass are requested before this one's sums are waited for
         if (r0 + step < M) request(row + step);
-        s1 = wave_sum(s1);
-        s2 = wave_sum(s2);
+        s1 = lanes_sum<TPR>(s1);
+        s2 = lanes_sum<TPR>(s2);
         if (TPR > 64) {
             const int wave = threadIdx.x >> 6, w0 = g * kWavesRow;
             if ((threadIdx.x & 63) == 0) {
@@ -222,7 +234,19 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
         }
     }
     if (!GRAD) return;
-    // the row groups' sums, added in group order
+    // the row groups' sums, added in group order; a wave's four of 16 lanes first
+    constexpr int kSums = TPR == 16 ? THREADS / 64 : kGroups;
+    const int sum = TPR == 16 ? threadIdx.x >> 6 : g;
+    const bool holds = TPR != 16 || (threadIdx.x & 63) < 16;
+    if (TPR == 16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dw.v[e] += __shfl_xor(dw.v[e], 16);
+            db.v[e] += __shfl_xor(db.v[e], 16);
+            dw.v[e] += __shfl_xor(dw.v[e], 32);
+            db.v[e] += __shfl_xor(db.v[e], 32);
+        }
+    }
     extern __shared__ float sums[];  // [2][n], where there is more than one group
     float *out_w = part + (int64_t)blockIdx.x * 2 * n, *out_b = out_w + n;
     if (gridDim.x == 1) {  // nothing to add to
@@ -230,8 +254,8 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
         out_b = dbias;
     }
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        if (g == k && c < len) {
+    for (int k = 0; k < kSums; ++k) {
+        if (sum == k && holds && c < len) {
             if (k > 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -240,7 +264,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
                     db.v[e] += sums[len + c + e];
                 }
             }
-            if (k + 1 < kGroups) {
+            if (k + 1 < kSums) {
                 store8(sums + c, n - c, dw);
                 store8(sums + len + c, n - c, db);
             } else {
@@ -248,7 +272,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
                 if (out_b) store8(out_b + c, n - c, db);
             }
         }
-        if (k + 1 < kGroups) __syncthreads();
+        if (k + 1 < kSums) __syncthreads();
     }
 }
 
@@ -338,6 +362,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restri
 // The threads a row of n takes, passed on as a template value.
 template <typename F>
 hipError_t held_shape(int64_t n, F f) {
+    if (n <= 128) return f(std::integral_constant<int, 16>());
     if (n <= 512) return f(std::integral_constant<int, 64>());
     if (n <= 1024) return f(std::integral_constant<int, 128>());
     if (n <= 2048) return f(std::integral_constant<int, 256>());

@@ -11,7 +11,8 @@
 //
 // Bound: HBM (8 to 14 flops an element).  x (and dy) are read once and held in
 // registers over the reductions: a row is spread over TPR threads of 8 elements
-// each, TPR the smallest that holds n; 256 threads take 256 / TPR rows at a time.
+// each, TPR the smallest that holds n (16 lanes up to 128 columns: 131072 x 128 forward
+// 15 us, 42 with a wave a row); 256 threads take 256 / TPR rows at a time.
 // Rows wider than kMaxHeld go through a kernel that reads them again for each
 // reduction, from L2 (a thread with 16 elements held is slower: 4096 x 12288
 // forward 62 us against 44, backward 72 against 69).
@@ -42,19 +43,20 @@ constexpr int kMaxRowGroups = 512;
 constexpr int64_t kLaunchRows = 1 << 21;  // of a launch with a workgroup a row: its threads stay below 2^32
 constexpr int kStreamThreads = 1024;   // workgroup of a row wider than kMaxHeld
 
-// Sum of v over the 16 lanes of a row group, or over the wave, on every lane: 16
-// lanes by rotations within them.
+// Sum of v over the 16 or 32 lanes of a row group, or over the wave, on every lane:
+// 16 lanes by rotations within them.
 template <int TPR>
 __device__ __forceinline__ float lanes_sum(float v) {
-    if (TPR != 16) return wave_sum(v);
+    if (TPR >= 64) return wave_sum(v);
     v += dpp_or<0x128, 0xF>(v, v);
     v += dpp_or<0x124, 0xF>(v, v);
     v += dpp_or<0x122, 0xF>(v, v);
     v += dpp_or<0x121, 0xF>(v, v);
+    if (TPR == 32) v += __shfl_xor(v, 16);
     return v;
 }
 
-// Sum of v over the TPR threads of a row group (16, or a multiple of 64); every
+// Sum of v over the TPR threads of a row group (16, 32 or a multiple of 64); every
 // thread of the workgroup calls it.  red: one float for each wave, not written
 // again before another barrier.
 template <int TPR>
@@ -234,46 +236,54 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
         }
     }
     if (!GRAD) return;
-    // the row groups' sums, added in group order; a wave's four of 16 lanes first
-    constexpr int kSums = TPR == 16 ? THREADS / 64 : kGroups;
-    const int sum = TPR == 16 ? threadIdx.x >> 6 : g;
-    const bool holds = TPR != 16 || (threadIdx.x & 63) < 16;
-    if (TPR == 16) {
+    // the row groups' sums: those of one wave first, then the others' in order, by the
+    // last one's threads (one after the other, each adding to LDS, cost 8 us a launch)
+    constexpr int kSums = TPR < 64 ? THREADS / 64 : kGroups;
+    const int sum = TPR < 64 ? threadIdx.x >> 6 : g;
+#pragma unroll
+    for (int o = TPR; o < 64; o *= 2) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            dw.v[e] += __shfl_xor(dw.v[e], 16);
-            db.v[e] += __shfl_xor(db.v[e], 16);
-            dw.v[e] += __shfl_xor(dw.v[e], 32);
-            db.v[e] += __shfl_xor(db.v[e], 32);
+            dw.v[e] += __shfl_xor(dw.v[e], o);
+            db.v[e] += __shfl_xor(db.v[e], o);
         }
     }
-    extern __shared__ float sums[];  // [2][n], where there is more than one group
+    const bool holds = c < len && (TPR >= 64 || (threadIdx.x & 63) < TPR);
+    extern __shared__ __attribute__((aligned(16))) float sums[];  // [kSums - 1][2][pitch]
+    const int pitch = (len + 7) / 8 * 8;
+    if (holds && sum + 1 < kSums) {
+        f32x4 *to = reinterpret_cast<f32x4 *>(sums + sum * 2 * pitch + c);
+        to[0] = f32x4{dw.v[0], dw.v[1], dw.v[2], dw.v[3]};
+        to[1] = f32x4{dw.v[4], dw.v[5], dw.v[6], dw.v[7]};
+        to += pitch / 4;
+        to[0] = f32x4{db.v[0], db.v[1], db.v[2], db.v[3]};
+        to[1] = f32x4{db.v[4], db.v[5], db.v[6], db.v[7]};
+    }
+    if (kSums > 1) __syncthreads();
+    if (!holds || sum + 1 < kSums) return;
+    f32x4 w0 = {}, w1 = {}, b0 = {}, b1 = {};
+#pragma unroll
+    for (int k = 0; k + 1 < kSums; ++k) {
+        const f32x4 *from = reinterpret_cast<const f32x4 *>(sums + k * 2 * pitch + c);
+        w0 += from[0];
+        w1 += from[1];
+        b0 += from[pitch / 4];
+        b1 += from[pitch / 4 + 1];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        dw.v[e] += w0[e];
+        dw.v[4 + e] += w1[e];
+        db.v[e] += b0[e];
+        db.v[4 + e] += b1[e];
+    }
     float *out_w = part + (int64_t)blockIdx.x * 2 * n, *out_b = out_w + n;
     if (gridDim.x == 1) {  // nothing to add to
         out_w = dweight;
         out_b = dbias;
     }
-#pragma unroll
-    for (int k = 0; k < kSums; ++k) {
-        if (sum == k && holds && c < len) {
-            if (k > 0) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (c + e >= len) continue;
-                    dw.v[e] += sums[c + e];
-                    db.v[e] += sums[len + c + e];
-                }
-            }
-            if (k + 1 < kSums) {
-                store8(sums + c, n - c, dw);
-                store8(sums + len + c, n - c, db);
-            } else {
-                if (out_w) store8(out_w + c, n - c, dw);
-                if (out_b) store8(out_b + c, n - c, db);
-            }
-        }
-        if (k + 1 < kSums) __syncthreads();
-    }
+    if (out_w) store8(out_w + c, n - c, dw);
+    if (out_b) store8(out_b + c, n - c, db);
 }
 
 // Wide rows' dX: one workgroup a row, read twice.
@@ -363,6 +373,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *__restri
 template <typename F>
 hipError_t held_shape(int64_t n, F f) {
     if (n <= 128) return f(std::integral_constant<int, 16>());
+    if (n <= 256) return f(std::integral_constant<int, 32>());
     if (n <= 512) return f(std::integral_constant<int, 64>());
     if (n <= 1024) return f(std::integral_constant<int, 128>());
     if (n <= 2048) return f(std::integral_constant<int, 256>());
@@ -397,7 +408,8 @@ hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, 
             constexpr int kTpr = decltype(tpr)::value, kThreads = kTpr > 512 ? kTpr : kGradThreads, kRows = kThreads / kTpr;
             const int64_t groups = (M + kRows - 1) / kRows;
             parts = groups < kMaxPartials ? (int)groups : kMaxPartials;
-            const size_t lds = kRows > 1 ? 2 * sizeof(float) * (size_t)n : 0;  // up to 32 KiB
+            constexpr int kSums = kTpr < 64 ? kThreads / 64 : kRows;
+            const size_t lds = 2 * sizeof(float) * (size_t)(kSums - 1) * (size_t)((n + 7) / 8 * 8);  // up to 60 KiB
             norm_bwd_kernel<T, W, kThreads, kTpr, true>
                 <<<parts, kThreads, lds, s>>>(x, dy, M, n, ldx, mean, rstd, w, dx, part, dw, db);
             return hipGetLastError();

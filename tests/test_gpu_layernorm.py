@@ -86,7 +86,8 @@ def test_widths(n, dtype):
 
 
 @pytest.mark.parametrize("rows,n", [(300, 64), (4200, 130), (1500, 1025), (700, 2750), (600, 4099), (300, 8192),
-                                    (270, 9001), (260, 16500)])
+                                    (270, 9001), (260, 16500), (5000, 8), (333, 17), (9000, 128), (77, 129), (2100, 255),
+                                    (700, 256), (41, 257)])
 def test_many_rows(rows, n):
     """More rows than the first pass of the workgroups takes, and than the partial rows."""
     check(rows, n, torch.bfloat16, torch.float32, rows + n)

@@ -148,6 +148,14 @@ __device__ __forceinline__ void transfer4(__amdgpu_buffer_rsrc_t r, uint32_t dst
         r, reinterpret_cast<__attribute__((address_space(3))) void *>(dst), 4, voff, 0, 0, 0);
 }
 
+// The barrier that hands a tile over: the wave's own transfers have arrived (a barrier
+// orders LDS accesses, not transfers that are still on their way), then everybody's.
+// Also where a wave has nothing to compute between its transfers and the barrier.
+__device__ __forceinline__ void tile_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    __syncthreads();
+}
+
 // The transfers of a wave: its quarter of a tile of ROWS rows, kRows at a time.
 // The chunk that a lane brings differs between its rows by an exclusive or with
 // the row group's number.  KEEP: the offsets stay in registers over the kernel;
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     // B: the buffer that tile j is in, a constant so that it is part of the instructions' offsets
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
-        __syncthreads();  // tile j is in LDS, and nobody reads the other buffer
+        tile_barrier();  // tile j is in LDS, and nobody reads the other buffer
         const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
         if (j + 1 < tiles) {
             mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
@@ -445,7 +453,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     }
     sum = pair_sum(sum);
     float *mine = team.slot(tiles_, 0);
-    __syncthreads();  // the tiles are read
+    tile_barrier();  // the tiles are read
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
         meet[0][threadIdx.x] = m;
@@ -530,7 +538,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
     const float c = a.scale * kLog2e;
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
-        __syncthreads();
+        tile_barrier();
         const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
         if (j + 1 < tiles) {
             mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
@@ -572,7 +580,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
     float *mine = team.slot(tiles_, 0);
-    __syncthreads();  // the tiles are read
+    tile_barrier();  // the tiles are read
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
         __syncthreads();
@@ -679,7 +687,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
     const int per = (at.end - at.first + kTile - 1) / kTile, tiles = per * (SPLIT ? 1 : group);
     auto tile_step = [&](int j, auto buf) {
         constexpr int B = decltype(buf)::value;
-        __syncthreads();
+        tile_barrier();
         int next_hd = hd, next_r0 = r0 + kTile;
         if (next_r0 >= at.end) {
             ++next_hd;
@@ -737,7 +745,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
     }
     // dk is the first part's to add and store, dv the second's, one after the other
     float *mine = team.slot(lds_, 0);
-    __syncthreads();  // the tiles are read
+    tile_barrier();  // the tiles are read
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(lds_, part - 1) + l, ak);
         __syncthreads();

@@ -231,6 +231,78 @@ struct Reader {
     }
 };
 
+// NaN and infinity keep to the causal order.  A masked p or ds is 0, but its product still
+// meets the other operand's row, and 0 times NaN is NaN.  So a workgroup whose results are
+// not all finite forms them once more, in a loop of its own: tiles that have masked places
+// enter those products with their finite values alone, and what the others give to the
+// rows that take them is added to the stored results (a running sum: the order is
+// causal).  Finite results have the same bits either way; where all are finite this
+// costs the look at them (us, without / with: 8192 rows forward 507 / 512, 4 x 1024 forward
+// and backward 228 / 232, (700, 3, 517, 1, 250, 1025) 12 / 4 D 64 62 / 64).
+template <int N>
+__device__ __forceinline__ bool not_finite(const f32x16 *t) {
+    float z[N] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int dt = 0; dt < N; ++dt) z[dt] = fmaf(t[dt][i], 0.0f, z[dt]);
+#pragma unroll
+    for (int dt = 1; dt < N; ++dt) z[0] += z[dt];
+    return z[0] != z[0];
+}
+// A tile of COUNT elements to another place in LDS (or its own), by the whole workgroup;
+// finite_only: zeros for the others.
+template <int COUNT>
+__device__ __forceinline__ void copy_tile(uint32_t to, uint32_t from, bool finite_only) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < COUNT / 8; i += blockDim.x) {
+        u32x4 w = *reinterpret_cast<const lds_u32x4 *>(from + i * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (finite_only && (w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+            if (finite_only && (w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+        }
+        *reinterpret_cast<lds_u32x4 *>(to + i * 16) = w;
+    }
+}
+// One wave: adds to its stored rows [first, last) of y, two columns a lane, what is not
+// finite in the rows of x that they take: those from `start` up to the row itself, or (DOWN)
+// from the row itself up to `start`, which is left out; of `heads` matrices, D columns
+// apart.  Weights are positive, so that an infinity keeps its sign; SIGNED: NaN instead.
+template <bool DOWN, bool SIGNED, typename Y>
+__device__ __forceinline__ void add_not_finite(Y *y, int64_t ldy, int first, int last, const uint16_t *x, int64_t ldx,
+                                               int heads, int start, int D) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the rows are stored
+    __threadfence_block();
+    const int c = 2 * (threadIdx.x & 63);
+    if (c >= D) return;
+    auto term = [](uint32_t bits) {
+        return (bits & 0x7F800000u) != 0x7F800000u ? 0.0f : SIGNED ? NAN : __uint_as_float(bits);
+    };
+    float sum0 = 0.0f, sum1 = 0.0f;
+    const int rows = DOWN ? start - first : last - start;
+#pragma unroll 1
+    for (int n = 0; n < rows; ++n) {
+        const int i = DOWN ? start - 1 - n : start + n;
+#pragma unroll 1
+        for (int hd = 0; hd < heads; ++hd) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(x + (int64_t)i * ldx + hd * D + c);
+            sum0 += term(w << 16);
+            sum1 += term(w & 0xFFFF0000u);
+        }
+        if (i < first || i >= last || (sum0 == 0.0f && sum1 == 0.0f)) continue;
+        Y *at = y + (int64_t)i * ldy + c;
+        if constexpr (sizeof(Y) == 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(at);
+            *reinterpret_cast<uint32_t *>(at) =
+                pack_bf16x2(__uint_as_float(w << 16) + sum0, __uint_as_float(w & 0xFFFF0000u) + sum1);
+        } else {
+            at[0] += sum0;
+            at[1] += sum1;
+        }
+    }
+}
+
 // A wave's 32 rows as fragments in registers: row l % 32, zeros past `end` and D.
 template <int DP>
 __device__ __forceinline__ void load_rows(const uint16_t *x, int64_t ld, int row0, int end, int D, bf16x8 *f) {
@@ -355,6 +427,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStep * DP];
     uint16_t(*ks_)[kStep * DP] = tiles_, (*vs_)[kStep * DP] = tiles_ + 2;
     __shared__ float meet[2][PARTS > 1 ? 64 * PARTS * GROUPS : 1];
+    __shared__ int odd;  // a result is not finite
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     // the long rows' tiles first
     const Place at = place_of<OWN>(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
@@ -378,26 +451,24 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     bf16x8 qf[DP / 16];
     load_rows<DP>(q + (int64_t)head * a.D, a.ldq, row0, at.end, a.D, qf);
     f32x16 acc[DP / 32];
-#pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
-    float m = -INFINITY, sum = 0.0f;
+    float m, sum;
     const float c = a.scale * kLog2e;
     const int tiles = (last - at.begin + kStep - 1) / kStep;
-    mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
-    mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
-    // B: the buffer that tile j is in, a constant so that it is part of the instructions' offsets
-    auto tile_step = [&](int j, auto buf) {
-        constexpr int B = decltype(buf)::value;
-        tile_barrier();  // tile j is in LDS, and nobody reads the other buffer
-        const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
-        if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
-            mv.load(vh, a.ldv, a.D, tile0 + kStep, at.end, lds_addr(vs_[1 - B]));
-        }
+    auto load = [&](int tile0, int b) {
+        mk.load(kh, a.ldk, a.D, tile0, at.end, lds_addr(ks_[b]));
+        mv.load(vh, a.ldv, a.D, tile0, at.end, lds_addr(vs_[b]));
+    };
+    auto start = [&] {
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
+        m = -INFINITY;
+        sum = 0.0f;
+    };
+    auto products = [&](int tile0, const uint32_t kt_, const uint32_t vt_) __attribute__((always_inline)) {
+        const int key0 = tile0 + kShare * part;
         if (key0 > row0 + 31) return;  // the wave's rows all come before this tile
-        const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
         f32x16 s[kShare / 32];
 #pragma unroll
         for (int t = 0; t < kShare / 32; ++t) {
@@ -447,13 +518,41 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
             for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(vt_, dt, st), p, acc[dt]);
         }
     };
+    // B: the buffer that tile j is in, a constant so that it is part of the instructions' offsets
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
+        tile_barrier();  // tile j is in LDS, and nobody reads the other buffer
+        const int tile0 = at.begin + j * kStep;
+        if (j + 1 < tiles) load(tile0 + kStep, 1 - B);
+        products(tile0, lds_addr(ks_[B]), lds_addr(vs_[B]));
+    };
+    if (threadIdx.x == 0) odd = 0;
+    load(at.begin, 0);
+    start();
     for (int j = 0; j < tiles; j += 2) {
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
+    if (not_finite<DP / 32>(acc)) odd = 1;
+    tile_barrier();  // the tiles are read
+    const bool ordered = odd;
+    if (ordered) {
+        start();
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+            const int tile0 = at.begin + j * kStep;
+            load(tile0, 0);
+            tile_barrier();
+            if (tile0 + kStep > at.first) {
+                copy_tile<kStep * DP>(lds_addr(vs_[0]), lds_addr(vs_[0]), true);
+                __syncthreads();
+            }
+            products(tile0, lds_addr(ks_[0]), lds_addr(vs_[0]));
+            __syncthreads();
+        }
+    }
     sum = pair_sum(sum);
     float *mine = team.slot(tiles_, 0);
-    tile_barrier();  // the tiles are read
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
         meet[0][threadIdx.x] = m;
@@ -472,6 +571,9 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     }
     store_rows<DP>(mine, o + head * a.D, res ? res + head * a.D : nullptr, ldo, row0, at.end, a.D, acc, 1.0f / sum);
     if (h == 0 && row < at.end) lse[(int64_t)head * a.T + row] = m * a.scale + logf(sum);
+    if (ordered)
+        add_not_finite<false, false>(o + head * a.D, ldo, row0, min(row0 + 32, at.end), vh, a.ldv, 1,
+                                     at.first - (at.first - at.begin) % kStep, a.D);
 }
 
 // dq, and the rows' statistics for the dk, dv kernel.
@@ -484,6 +586,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
     constexpr int OWN = 32 * GROUPS, kShare = PARTS == 1 ? 64 : 32, kStep = kShare * PARTS;
     __shared__ __attribute__((aligned(256))) uint16_t tiles_[4][kStep * DP];
     uint16_t(*ks_)[kStep * DP] = tiles_, (*vs_)[kStep * DP] = tiles_ + 2;
+    __shared__ int odd;  // a result is not finite
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
     const Place at = place_of<OWN>(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
@@ -502,8 +605,12 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
     rd.init(kShare * part);
     const uint16_t *kh = k + (int64_t)kv * a.D, *vh = v + (int64_t)kv * a.D;
     const int tiles = (last - at.begin + kStep - 1) / kStep;
-    mk.load(kh, a.ldk, a.D, at.begin, at.end, lds_addr(ks_[0]));
-    mv.load(vh, a.ldv, a.D, at.begin, at.end, lds_addr(vs_[0]));
+    auto load = [&](int tile0, int b) {
+        mk.load(kh, a.ldk, a.D, tile0, at.end, lds_addr(ks_[b]));
+        mv.load(vh, a.ldv, a.D, tile0, at.end, lds_addr(vs_[b]));
+    };
+    if (threadIdx.x == 0) odd = 0;
+    load(at.begin, 0);
     bf16x8 qf[DP / 16], df[DP / 16];
     load_rows<DP>(q + (int64_t)head * a.D, a.ldq, row0, at.end, a.D, qf);
     load_rows<DP>(dout + (int64_t)head * a.D, ldo, row0, at.end, a.D, df);
@@ -531,20 +638,16 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
         stats[(int64_t)(a.H + head) * a.T + row] = dl;
     }
     f32x16 acc[DP / 32];
-#pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
     const float c = a.scale * kLog2e;
-    auto tile_step = [&](int j, auto buf) {
-        constexpr int B = decltype(buf)::value;
-        tile_barrier();
-        const int tile0 = at.begin + j * kStep, key0 = tile0 + kShare * part;
-        if (j + 1 < tiles) {
-            mk.load(kh, a.ldk, a.D, tile0 + kStep, at.end, lds_addr(ks_[1 - B]));
-            mv.load(vh, a.ldv, a.D, tile0 + kStep, at.end, lds_addr(vs_[1 - B]));
-        }
-        const uint32_t kt_ = lds_addr(ks_[B]), vt_ = lds_addr(vs_[B]);
+    auto start = [&] {
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
+    };
+    // kc_: the keys' tile that ds is multiplied with
+    auto products = [&](int tile0, const uint32_t kt_, const uint32_t vt_, const uint32_t kc_) __attribute__((always_inline)) {
+        const int key0 = tile0 + kShare * part;
 #pragma unroll
         for (int t = 0; t < kShare / 32; ++t) {
             const int k0 = key0 + 32 * t;
@@ -563,7 +666,10 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
             if (k0 + 31 > row0) {  // a branch: most tiles have nothing to mask
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (k0 + tile_row(i) > row - 4 * h) s[i] = -INFINITY;
+                    if (k0 + tile_row(i) > row - 4 * h) {
+                        s[i] = -INFINITY;
+                        dp[i] = 0.0f;
+                    }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
@@ -571,16 +677,39 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
             for (int st = 0; st < 2; ++st) {
                 const bf16x8 ds = operand_of(s, st);
 #pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(kt_, dt, 2 * t + st), ds, acc[dt]);
+                for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(rd.cols(kc_, dt, 2 * t + st), ds, acc[dt]);
             }
         }
     };
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
+        tile_barrier();
+        const int tile0 = at.begin + j * kStep;
+        if (j + 1 < tiles) load(tile0 + kStep, 1 - B);
+        products(tile0, lds_addr(ks_[B]), lds_addr(vs_[B]), lds_addr(ks_[B]));
+    };
+    start();
     for (int j = 0; j < tiles; j += 2) {
         tile_step(j, std::integral_constant<int, 0>());
         if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
     }
-    float *mine = team.slot(tiles_, 0);
+    if (not_finite<DP / 32>(acc)) odd = 1;
     tile_barrier();  // the tiles are read
+    const bool ordered = odd;
+    if (ordered) {
+        start();
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+            const int tile0 = at.begin + j * kStep;
+            load(tile0, 0);
+            tile_barrier();
+            copy_tile<kStep * DP>(lds_addr(ks_[1]), lds_addr(ks_[0]), tile0 + kStep > at.first);
+            __syncthreads();
+            products(tile0, lds_addr(ks_[0]), lds_addr(vs_[0]), lds_addr(ks_[1]));
+            __syncthreads();
+        }
+    }
+    float *mine = team.slot(tiles_, 0);
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(tiles_, part - 1) + l, acc);
         __syncthreads();
@@ -589,6 +718,9 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dq_kernel(
         for (int p = 1; p < PARTS; ++p) add_tiles<DP / 32>(acc, 1.0f, team.slot(tiles_, p - 1) + l, 1.0f);
     }
     store_rows<DP>(mine, dq + head * a.D, nullptr, lddq, row0, at.end, a.D, acc, a.scale);
+    if (ordered)
+        add_not_finite<false, true>(dq + head * a.D, lddq, row0, min(row0 + 32, at.end), kh, a.ldk, 1,
+                                    at.first - (at.first - at.begin) % kStep, a.D);
 }
 
 // Where the dk, dv kernel's results go: the gradients, or with `part` one fp32
@@ -629,6 +761,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
     uint16_t(*qs_)[kTile * DP] = reinterpret_cast<uint16_t(*)[kTile * DP]>(lds_ + OWN * DP), (*ds_)[kTile * DP] = qs_ + 2;
     static_assert(PARTS == 1 || (PARTS - 1) * GROUPS * DP / 2 * 64 * 4 <= sizeof(lds_), "the parts' results");
     __shared__ __attribute__((aligned(16))) float ls_[2][kTile], dl_[2][kTile];
+    __shared__ int odd;  // a result is not finite
     const int group = a.H / a.Hk, heads = SPLIT ? a.H : a.Hk;
     const int first_head = SPLIT ? head_of(blockIdx.x % a.H, a.H, a.Hk) : (int)(blockIdx.x % a.Hk) * group;
     const int kv = first_head / group;
@@ -674,31 +807,26 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
         mk.init(a.ldk, a.D);
         mk.load(k + (int64_t)kv * a.D, a.ldk, a.D, at.first, at.end, lds_addr(ks_));
     }
+    if (threadIdx.x == 0) odd = 0;
     fetch(hd, r0, 0);
     bf16x8 vf[DP / 16];
     load_rows<DP>(v + (int64_t)kv * a.D, a.ldv, key0, at.end, a.D, vf);
     f32x16 ak[DP / 32], av[DP / 32];
+    auto start = [&] {
 #pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
+        for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.0f;
+    };
     const float c = a.scale * kLog2e;
     uint32_t kt_ = lds_addr(ks_) + 32 * (team.group - part) * DP * 2;  // the reader is 32 part rows ahead
     const int per = (at.end - at.first + kTile - 1) / kTile, tiles = per * (SPLIT ? 1 : group);
-    auto tile_step = [&](int j, auto buf) {
-        constexpr int B = decltype(buf)::value;
-        tile_barrier();
-        int next_hd = hd, next_r0 = r0 + kTile;
-        if (next_r0 >= at.end) {
-            ++next_hd;
-            next_r0 = at.first;
-        }
-        if (j + 1 < tiles) fetch(next_hd, next_r0, 1 - B);
-        const uint32_t qt_ = lds_addr(qs_[B]), dt_ = lds_addr(ds_[B]);
+    // The tile of rows from r0 on, in buffer B; C: the one whose columns p and ds are multiplied with
+    auto products = [&](int r0, auto buf, auto cols) __attribute__((always_inline)) {
+        constexpr int B = decltype(buf)::value, C = decltype(cols)::value;
+        const uint32_t qt_ = lds_addr(qs_[B]), dt_ = lds_addr(ds_[B]), qc_ = lds_addr(qs_[C]), dc_ = lds_addr(ds_[C]);
         const uint32_t lt_ = lds_addr(ls_[B]) + 16 * h + 128 * part, et_ = lds_addr(dl_[B]) + 16 * h + 128 * part;
         const int q0 = r0 + 32 * part;
-        hd = next_hd;
-        r0 = next_r0;
         if (q0 + 31 < key0) return;  // these rows all come before the wave's keys
         asm volatile("" : "+s"(kt_));  // read the keys again, do not keep their fragments over the loop
         f32x16 s, dp;
@@ -720,7 +848,10 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
         if (q0 < key0 + 31) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (q0 + tile_row(i) < key - 4 * h) s[i] = -INFINITY;
+                if (q0 + tile_row(i) < key - 4 * h) {
+                    s[i] = -INFINITY;
+                    dp[i] = 0.0f;
+                }
         }
         u32x4 pw[2], sw[2];
 #pragma unroll
@@ -734,18 +865,53 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
             const bf16x8 pb = __builtin_bit_cast(bf16x8, pw[st]), sb = __builtin_bit_cast(bf16x8, sw[st]);
 #pragma unroll
             for (int dt = 0; dt < DP / 32; ++dt) {
-                av[dt] = mfma(rd.cols(dt_, dt, st), pb, av[dt]);
-                ak[dt] = mfma(rd.cols(qt_, dt, st), sb, ak[dt]);
+                av[dt] = mfma(rd.cols(dc_, dt, st), pb, av[dt]);
+                ak[dt] = mfma(rd.cols(qc_, dt, st), sb, ak[dt]);
             }
         }
     };
+    typedef std::integral_constant<int, 0> Zero;
+    typedef std::integral_constant<int, 1> One;
+    auto next_tile = [&] {
+        r0 += kTile;
+        if (r0 >= at.end) {
+            ++hd;
+            r0 = at.first;
+        }
+    };
+    auto tile_step = [&](int j, auto buf) {
+        constexpr int B = decltype(buf)::value;
+        tile_barrier();
+        const int now = r0;
+        next_tile();
+        if (j + 1 < tiles) fetch(hd, r0, 1 - B);
+        products(now, buf, buf);
+    };
+    start();
     for (int j = 0; j < tiles; j += 2) {
-        tile_step(j, std::integral_constant<int, 0>());
-        if (j + 1 < tiles) tile_step(j + 1, std::integral_constant<int, 1>());
+        tile_step(j, Zero());
+        if (j + 1 < tiles) tile_step(j + 1, One());
+    }
+    if (not_finite<DP / 32>(ak) || not_finite<DP / 32>(av)) odd = 1;
+    tile_barrier();  // the tiles are read
+    const bool ordered = odd;
+    if (ordered) {
+        start();
+        hd = first_head;
+        r0 = at.first;
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j, next_tile()) {
+            fetch(hd, r0, 0);
+            tile_barrier();
+            copy_tile<kTile * DP>(lds_addr(qs_[1]), lds_addr(qs_[0]), r0 < at.first + OWN);
+            copy_tile<kTile * DP>(lds_addr(ds_[1]), lds_addr(ds_[0]), r0 < at.first + OWN);
+            __syncthreads();
+            products(r0, Zero(), One());
+            __syncthreads();
+        }
     }
     // dk is the first part's to add and store, dv the second's, one after the other
     float *mine = team.slot(lds_, 0);
-    tile_barrier();  // the tiles are read
     if (PARTS > 1) {
         if (part > 0) put_tiles<DP / 32>(team.slot(lds_, part - 1) + l, ak);
         __syncthreads();
@@ -766,6 +932,12 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_dkv_kernel(
         for (int p = 1; p < PARTS; ++p) add_tiles<DP / 32>(av, 1.0f, team.slot(lds_, p - 1) + l, 1.0f);
         if (SPLIT) store_rows_f32<DP>(pv, a.D, key0, at.end, a.D, av, 1.0f);
         else store_rows<DP>(mine, out.dv + kv * a.D, nullptr, out.lddv, key0, at.end, a.D, av, 1.0f);
+        if (ordered) {  // (dk has them: a row whose q, k, v or do is not finite has no finite ds)
+            const uint16_t *dh = dout + (int64_t)first_head * a.D;
+            const int end = min(key0 + 32, at.end), start = min(at.first + (OWN > kTile ? OWN : kTile), at.end);
+            if (SPLIT) add_not_finite<true, false>(pv, a.D, key0, end, dh, ldo, 1, start, a.D);
+            else add_not_finite<true, false>(out.dv + kv * a.D, out.lddv, key0, end, dh, ldo, group, start, a.D);
+        }
     }
 }
 

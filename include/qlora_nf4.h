@@ -445,8 +445,8 @@ typedef struct {
  *   lse    device fp32 [heads x T], written
  * All arrays but cu_seqlens and lse 16-byte aligned.  Scores and sums in fp32; the
  * weights are rounded to bf16 for their product with v.  The same bits on every run.
- * A NaN or infinity in a row of k or v may reach every row of its own sequence
- * (never of another).
+ * A NaN or infinity in a row of k or v reaches the rows that attend to it and no
+ * others; the backward's results likewise depend on no row that the order masks.
  * Errors: QLORA_EINVAL (null pointer, size <= 0, heads % kv_heads, a pitch below
  * its row, scale not positive and finite), QLORA_ENOTSUP (dim > 128 or not a
  * multiple of 8, scale < 2^-64, pitch not a multiple of 8 or above 2^23, T > 2^30, too many

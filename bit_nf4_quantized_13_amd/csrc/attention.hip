@@ -495,15 +495,15 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
         if (__ballot((top - m) * c > 8.0f)) {
             const float old = m;
             m = fmaxf(m, top);
-            // a second part may not have met a key that the row attends to
-            const float f = PARTS > 1 && m == old ? 1.0f : __builtin_amdgcn_exp2f((old - m) * c);
+            // no score above -inf yet: no key that the row attends to met by this part, or scores of -inf
+            const float f = m == old ? 1.0f : __builtin_amdgcn_exp2f((old - m) * c);
             sum *= f;
 #pragma unroll
             for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
         }
-        const float mc = PARTS > 1 && m == -INFINITY ? 0.0f : m * c;
+        const float mc = fmaxf(m * c, -0x1.fffffep127f);  // finite: p is 0 under it
 #pragma unroll
         for (int t = 0; t < kShare / 32; ++t)
 #pragma unroll

@@ -136,3 +136,22 @@ def test_other_sequences_keep_their_bits():
         keep[a:b] = False
         for key in got:
             assert torch.equal(got[key][keep.cuda()], clean[key][keep.cuda()]), key
+
+
+@pytest.mark.parametrize("t,h,hk,d", [(200, 2, 1, 64), (190, 2, 2, 128), (400, 2, 1, 64), (420, 80, 40, 72), (330, 160, 80, 64)])
+@pytest.mark.parametrize("low,scale", [(-INF, None), (torch.finfo(torch.bfloat16).min, 1.0)])
+def test_first_keys_ruled_out(t, h, hk, d, low, scale):
+    """Keys whose scores are -inf (or fall there once scaled), more of them than a tile: the later rows attend to
+    the other keys as if these were not there."""
+    say(f"attention order first keys at {low} T={t} heads={h}/{hk} dim={d}")
+    n = 133
+    q, k, v, do, cu = make([t], h, hk, d, t + 2)
+    q[:, :, 0] = 1.0
+    k[:, :, 0] = 0.0
+    want = run(q[n:].contiguous(), k[n:].contiguous(), v[n:].contiguous(), do[n:].contiguous(), torch.tensor([0, t - n]).int().cuda(), scale)
+    k[:n, :, 0] = low
+    got = run(q, k, v, do, cu, scale)
+    # o and lse of the two tilings: each within 2^-8 of a weighted mean of |v| (under 6) and of itself; scores below 60
+    assert float((got["o"][n:].float() - want["o"].float()).abs().max()) <= 4 * 6 * 2.0 ** -8
+    assert float((got["lse"][n:] - want["lse"]).abs().max()) <= 2 * 61 * 2.0 ** -12
+    assert bool(got["dv"][n:].isfinite().all())

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(THREADS) void logprob_piece_kernel(const T *__restr
     for (int i = tid; i < 8 * nvec; i += THREADS) {
         const float x1 = vals[i];
         const int c = at_c[i >> 3] + (i & 7);
-        if (c < left && (all || x1 >= thr)) cand[atomicAdd(&ncand, 1)] = key_of(x1, (uint32_t)(c0 + c));
+        if (c < left && (all ? x1 == x1 : x1 >= thr)) cand[atomicAdd(&ncand, 1)] = key_of(x1, (uint32_t)(c0 + c));  // no NaN
     }
     __syncthreads();
     const int n = ncand;

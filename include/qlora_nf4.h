@@ -493,7 +493,7 @@ size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top);
  * A logit of -inf is a token that is ruled out: p = 0.  A row of -inf alone has
  * lse = -inf, logp = -inf, entropy 0 and alternatives of -inf at the lowest
  * indices.  A NaN or +inf in a row makes its results NaN (logp without a target
- * stays 0; the alternatives are then the other logits, -1 where none are left).
+ * stays 0); the alternatives' indices never name a NaN: -1 where no other logit is left.
  * Errors: QLORA_EINVAL (null pointer, size <= 0, ld < V, top > V), QLORA_ENOTSUP
  * (unknown type, V > 2^19, top > 16, too many rows for one launch), QLORA_EALIGN,
  * QLORA_EWORKSPACE.

@@ -12,7 +12,9 @@
 // decades, and sqrt(v), which divides, has the resolution of m.  v > 0 never
 // becomes 0, so m is never divided by eps alone.  A block whose scale would be
 // below the smallest normal number is stored as zeros.  All of it is fixed
-// IEEE arithmetic: the codes are reproducible bit for bit.
+// IEEE arithmetic: the codes are reproducible bit for bit.  An element whose new m or v is
+// not finite is left out of the maxima, so that its block keeps its scales; m's code -128
+// marks it (v's is 0) and reads as NaN for both, as fp32 states would hold the damage.
 //
 // Bound: HBM, 24 bytes an element with fp32 states, 12 with 8-bit states (bf16
 // p, fp32 g).  Each thread takes 8 consecutive elements of every array (16-byte
@@ -83,13 +85,16 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int64_t cnt, const U8x8 
         if (i < cnt) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
 }
 
-__device__ __forceinline__ float decode_m(const U8x8 &r, int i, float scale) {
-    const float c = (float)(int8_t)(r.w[i >> 2] >> (8 * (i & 3)));
-    return c * fabsf(c) * scale;
-}
-__device__ __forceinline__ float decode_v(const U8x8 &r, int i, float scale) {
-    const float c = (float)(uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
-    return c * c * (c * c) * scale;
+constexpr int kLost = -128;  // m's code of an element whose states are not finite
+
+__device__ __forceinline__ void decode(const U8x8 &mc, const U8x8 &vc, float m_scale, float v_scale, F8 &m, F8 &v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int code = (int8_t)(mc.w[i >> 2] >> (8 * (i & 3)));
+        const float c = (float)code, d = (float)(uint8_t)(vc.w[i >> 2] >> (8 * (i & 3)));
+        m.v[i] = code == kLost ? NAN : c * fabsf(c) * m_scale;
+        v.v[i] = code == kLost ? NAN : d * d * (d * d) * v_scale;
+    }
 }
 
 // Maximum over the half wave that holds a block.
@@ -159,23 +164,12 @@ __device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyp
             v = load8((const float *)t.v + at, cnt);
         }
     }
-    if (BITS8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m.v[i] = decode_m(mc, i, ms0);
-            v.v[i] = decode_v(vc, i, vs0);
-        }
-    }
-    float mtop = 0.0f, vtop = 0.0f;
+    if (BITS8) decode(mc, vc, ms0, vs0, m, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float gi = g.v[i] * h.grad_scale;
         m.v[i] = m.v[i] * h.beta1 + gi * h.one_minus_beta1;
         v.v[i] = v.v[i] * h.beta2 + gi * gi * h.one_minus_beta2;
-        if (BITS8) {
-            mtop = fmaxf(mtop, fabsf(m.v[i]));
-            vtop = fmaxf(vtop, v.v[i]);
-        }
     }
     if (h.eps >= kFastEps) {
         // root and reciprocal to the last place each: the update's own error stays below 3 units of it
@@ -195,6 +189,16 @@ __device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyp
         store8((float *)t.m + at, FULL ? 8 : cnt, m);
         store8((float *)t.v + at, FULL ? 8 : cnt, v);
         return;
+    }
+    float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (!(fabsf(m.v[i]) < INFINITY && v.v[i] < INFINITY)) {
+            m.v[i] = NAN;  // which fmaxf leaves out
+            v.v[i] = 0.0f;
+        }
+        mtop = fmaxf(mtop, fabsf(m.v[i]));
+        vtop = fmaxf(vtop, v.v[i]);
     }
     const float ms = block_scale_of(block_max(mtop), kMUnit), vs = block_scale_of(block_max(vtop), kVUnit);
     const float mi = ms > 0.0f ? 1.0f / ms : 0.0f, vi = vs > 0.0f ? 1.0f / vs : 0.0f;
@@ -216,7 +220,7 @@ __device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyp
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         int c = (int)fminf(cm[i], 127.0f);
-        c = m.v[i] < 0.0f ? -c : c;
+        c = m.v[i] < 0.0f ? -c : m.v[i] != m.v[i] ? kLost : c;
         mc.w[i >> 2] |= (uint32_t)(uint8_t)c << (8 * (i & 3));
         int d = (int)fminf(cv[i], 255.0f);
         if (v.v[i] > 0.0f && vs > 0.0f && d < 1) d = 1;
@@ -249,11 +253,7 @@ __global__ __launch_bounds__(kThreads) void adamw_moments_kernel(TensorList list
     const U8x8 mc = load_codes((const uint8_t *)t.m + at, cnt), vc = load_codes((const uint8_t *)t.v + at, cnt);
     const float ms = t.m_scale[at >> 8], vs = t.v_scale[at >> 8];
     F8 m, v;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m.v[i] = decode_m(mc, i, ms);
-        v.v[i] = decode_v(vc, i, vs);
-    }
+    decode(mc, vc, ms, vs, m, v);
     store8((float *)t.param + at, cnt, m);
     store8((float *)const_cast<void *>(t.grad) + at, cnt, v);
 }

@@ -554,6 +554,8 @@ typedef struct {
  *                                        and c >= 1 where v > 0
  * (IEEE fp32 operations; a scale below the smallest normal number becomes 0
  * and its block zeros).  Zeroed codes and scales are the states at the start.
+ * An element whose new m or v is not finite does not count for the scales; its codes
+ * are m's -128 and v's 0, which stand for NaN in both (its weight is NaN from the next step on).
  * Errors: QLORA_EINVAL (null pointer, n < 0, step < 1, a rate out of range,
  * master without use_master or the reverse, use_master with fp32 param),
  * QLORA_ENOTSUP (unknown type, n > 2^34), QLORA_EALIGN.

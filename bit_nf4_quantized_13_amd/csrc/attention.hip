@@ -976,18 +976,27 @@ bool split_heads(const AttentionShape &a) {
 }
 
 // Parts, from the mean length L of the sequences (the lengths themselves are on the
-// device) and the T H rows of all heads.  Four, with 64 rows a workgroup instead of 128,
-// where these run in one round (their LDS leaves one a CU for D > 64, two below), or
-// one long sequence is most of it.  Forward + backward, one part / two / four (us): 1 x 1024 H / Hk 8 / 8 D 128
-// 109 / 83 / 64, 2 x 512 16 / 16 D 128 59 / 58 / 51, (1000, 20, 20, 20, 20) 8 / 4 D 64 69 / 58 / 43, 4 x 256 8 / 8
-// D 128 40 / 43 / 41; beyond: 3 x 512 16 / 16 D 128 63 / 61 / 83, 8 x 128 16 / 4 D 128 45 / 51 / 52.
+// device) and the T H rows of all heads, which make T H / 64 workgroups of four parts.
+// Four where these run in one round: LDS leaves one a CU for D > 64, registers one in the
+// backward (150 to 160: three waves a SIMD, a workgroup takes two); forward for D <= 64 two.
+// Or where one long sequence is most of it.  Forward + backward, one part / two / four (us):
+// 1 x 1024 H / Hk 8 / 8 D 128 94 / 82 / 64, 2 x 512 16 / 16 D 128 60 / 58 / 50, (1000, 20, 20, 20, 20) 8 / 4 D 64
+// 69 / 58 / 43, 4 x 256 8 / 8 D 128 40 / 43 / 40; beyond: 3 x 512 16 / 16 D 128 63 / 60 / 83, 8 x 128 16 / 4 D 128
+// 45 / 51 / 52.  D = 64, T H from 16384 to 32768, forward alone: (700, 3, 517, 1, 250, 1025) 12 / 4 20 / 19 / 16,
+// 1 x 2048 16 / 4 31 / 25 / 20, 4 x 512 12 / 12 11.7 / 10.8 / 12.2, 6 x 300 14 / 14 9.4 / 10.7 / 11.2 (what equal
+// lengths lose is less than what others gain); backward alone, T H up to 32 L: 1 x 1024 20 / 20 48 / 41 / 34,
+// 1 x 2048 16 / 4 94 / 74 / 64, 1 x 768 32 / 32 39 / 34 / 34; beyond: 4 x 512 12 / 12 31 / 29 / 36, 6 x 300 14 / 14
+// 25 / 24 / 35, 8 x 256 16 / 16 24 / 24 / 34, the batch of 12 / 4 58 / 52 / 51, (3000, 9 times 20) 9 / 3 126 / 95 / 76.
 // Two, of 128 rows, where the workgroups are no more than the 512 that run at a time
 // with one part: 1 x 8192 8 / 2 D 128 812 / 645, 2 x 2048 16 / 16 D 64 174 / 137, (2570, 37, 34, 0, 110, 2, 14, 5)
-// 8 / 8 D 128 204 / 169; beyond: 4 x 512 32 / 32 D 64 67 / 75, 1 x 8192 16 / 4 D 128 1228 / 1267.
-int parts_of(const AttentionShape &a) {
+// 8 / 8 D 128 204 / 169; beyond: 4 x 512 32 / 32 D 64 67 / 75, 1 x 8192 16 / 4 D 128 1228 / 1267.  Shorter sequences
+// where a backward's are one a CU: D 64 8 x 210 14 / 14 25 / 21, 8 x 256 12 / 4 36 / 31, 7 x 280 14 / 14 30 / 35.
+int parts_of(const AttentionShape &a, bool backward) {
     const int64_t len = a.T / a.S, rows = (int64_t)a.T * a.H;
-    const bool one_round = rows <= (a.D <= 64 ? 32768 : 16384), one_long = rows <= 32768 && rows <= 12 * len;
-    if (len >= 200 && (one_round || one_long)) return 4;
+    const bool narrow = a.D <= 64, half = rows <= 32768;
+    const bool one_round = rows <= 16384 || (narrow && !backward && half);
+    if (len >= 200 && (one_round || (half && rows <= (narrow ? 32 : 12) * len))) return 4;
+    if (len >= 200 && narrow && backward && half) return 2;
     return len >= 300 && rows <= 65536 && rows <= 80 * len ? 2 : 1;
 }
 size_t stats_bytes(const AttentionShape &a) { return (sizeof(float) * 2 * (size_t)a.T * a.H + 255) / 256 * 256; }
@@ -1016,9 +1025,9 @@ hipError_t backward(const AttentionShape &a, const uint16_t *q, const uint16_t *
 
 // f with the padded head dimension, the parts and the groups as template values.
 template <typename F>
-hipError_t shaped(const AttentionShape &a, F f) {
+hipError_t shaped(const AttentionShape &a, bool backward, F f) {
     auto with = [&](auto dp) {
-        switch (parts_of(a)) {
+        switch (parts_of(a, backward)) {
             case 4: return f(dp, std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
             case 2: return f(dp, std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
             default: return f(dp, std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
@@ -1037,7 +1046,7 @@ size_t attention_bwd_bytes(const AttentionShape &a) {
 
 hipError_t launch_attention_fwd(const AttentionShape &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                 const int32_t *cu, uint16_t *o, uint16_t *res, float *lse, hipStream_t s) {
-    return shaped(a, [&](auto dp, auto parts, auto groups) {
+    return shaped(a, false, [&](auto dp, auto parts, auto groups) {
         constexpr int kDp = decltype(dp)::value, kParts = decltype(parts)::value, kGroups = decltype(groups)::value;
         const int slots = slots_of(a, 32 * kGroups);
         attention_fwd_kernel<kDp, kParts, kGroups>
@@ -1052,7 +1061,7 @@ hipError_t launch_attention_bwd(const AttentionShape &a, const uint16_t *q, cons
                                 uint16_t *dv, int64_t lddv, void *ws, hipStream_t s) {
     float *stats = static_cast<float *>(ws);
     const KvOut out{dk, dv, lddk, lddv, reinterpret_cast<float *>(static_cast<char *>(ws) + stats_bytes(a))};
-    return shaped(a, [&](auto dp, auto parts, auto groups) {
+    return shaped(a, true, [&](auto dp, auto parts, auto groups) {
         return backward<decltype(dp)::value, decltype(parts)::value, decltype(groups)::value>(a, q, k, v, o, res, lse, dout, cu, dq, lddq, stats, out, s);
     });
 }

@@ -159,13 +159,13 @@ __global__ __launch_bounds__(kStreamThreads) void norm_fwd_stream_kernel(
     }
 }
 
-// dX, and with GRAD the workgroup's partial row of dw and db ([2][n] at
+// dX (which may be written over dy), and with GRAD the workgroup's partial row of dw and db ([2][n] at
 // part + blockIdx.x 2 n).  Row group g of the workgroup takes the rows
 // blockIdx.x GROUPS + g, then every gridDim.x GROUPS-th.
 template <typename T, typename W, int THREADS, int TPR, bool GRAD>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
-    const T *__restrict__ x, const T *__restrict__ dy, int64_t M, int64_t n, int64_t ldx,
-    const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx,
+    const T *__restrict__ x, const T *dy, int64_t M, int64_t n, int64_t ldx,
+    const float *__restrict__ mean, const float *__restrict__ rstd, const W *__restrict__ w, T *dx,
     float *__restrict__ part, float *__restrict__ dweight, float *__restrict__ dbias) {
     constexpr int kGroups = THREADS / TPR, kWavesRow = TPR / 64;
     __shared__ float red[2][2][THREADS / 64];  // of the two sums, in turn from one pass over the rows to the next
@@ -291,8 +291,8 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(
 // Wide rows' dX: one workgroup a row, read twice.
 template <typename T, typename W>
 __global__ __launch_bounds__(kStreamThreads) void norm_bwd_stream_kernel(
-    const T *__restrict__ x, const T *__restrict__ dy, int64_t n, int64_t ldx, const float *__restrict__ mean,
-    const float *__restrict__ rstd, const W *__restrict__ w, T *__restrict__ dx) {
+    const T *__restrict__ x, const T *dy, int64_t n, int64_t ldx, const float *__restrict__ mean,
+    const float *__restrict__ rstd, const W *__restrict__ w, T *dx) {
     __shared__ float red1[kStreamThreads / 64], red2[kStreamThreads / 64];
     const int64_t row = blockIdx.x;
     const T *xr = x + row * ldx, *dr = dy + row * n;
@@ -426,17 +426,17 @@ hipError_t norm_bwd(const T *x, const T *dy, int64_t M, int64_t n, int64_t ldx, 
         });
     } else {
         e = hipSuccess;
+        if (grad) {  // before dx, which may overwrite dy
+            parts = M < kMaxPartials ? (int)M : kMaxPartials;
+            norm_cols_kernel<T><<<dim3((unsigned)((n + 2047) / 2048), parts), 256, 0, s>>>(x, dy, M, n, ldx, mean, rstd, part);
+            e = hipGetLastError();
+        }
         for (int64_t r = 0; r < M && e == hipSuccess; r += kLaunchRows) {
             const int64_t rows = M - r < kLaunchRows ? M - r : kLaunchRows;
             norm_bwd_stream_kernel<T, W><<<(unsigned)rows, kStreamThreads, 0, s>>>(x + r * ldx, dy + r * n, n, ldx, mean + r, rstd + r,
                                                                                   w, dx + r * n);
             e = hipGetLastError();
         }
-    }
-    if (grad && !fused && e == hipSuccess) {
-        parts = M < kMaxPartials ? (int)M : kMaxPartials;
-        norm_cols_kernel<T><<<dim3((unsigned)((n + 2047) / 2048), parts), 256, 0, s>>>(x, dy, M, n, ldx, mean, rstd, part);
-        e = hipGetLastError();
     }
     if (!grad || e != hipSuccess || (fused && parts == 1)) return e;
     norm_reduce_kernel<<<(unsigned)((2 * n + 63) / 64), 1024, 0, s>>>(part, parts, n, dw, db);

@@ -410,7 +410,7 @@ size_t qlora_layernorm_workspace(int64_t M, int64_t n);
  *   dx = rstd (g - mean(g) - xh mean(g xh))    dweight = sum over rows of dy xh
  *   dbias = sum over rows of dy
  *   x, weight as in the forward; mean, rstd its outputs
- *   dy      device [M x n] of x_type, dense;  dx likewise, written
+ *   dy      device [M x n] of x_type, dense;  dx likewise, written; may be dy (in place)
  *   dweight, dbias  device fp32 [n], written, or NULL to skip them (a frozen norm)
  *   ws      >= qlora_layernorm_workspace(M, n) bytes with dweight or dbias, else unused.
  * Rows are added in a fixed order: the same bits on every run.

@@ -32,7 +32,6 @@ int check_norm(const void *x, int32_t x_type, int64_t M, int64_t n, int64_t ldx,
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // row numbers and tile ends stay below 2^31
 constexpr float kMinScale = 0x1p-64f;             // lse / scale stays far from overflow
-constexpr int64_t kMaxPitch = int64_t(1) << 23;   // 64 rows of a tile lie within 2^30 bytes
 
 // A matrix of `width` values a row: pitch and alignment of 16-byte accesses.
 int check_pitch(int64_t ld, int64_t width) {

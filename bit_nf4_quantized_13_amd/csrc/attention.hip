@@ -164,11 +164,12 @@ __device__ __forceinline__ void tile_barrier() {
 template <int DP, int ROWS, int WAVES, bool KEEP>
 struct Mover {
     static constexpr int kChunks = DP / 8, kRows = 64 / kChunks, kOwnRows = ROWS / WAVES, kOps = kOwnRows / kRows;
+    static constexpr uint32_t kNowhere = 0x80000000u;  // past every tile's range
+    static_assert((int64_t)ROWS * kMaxPitch * 2 <= kNowhere, "a tile's rows, at the largest pitch");
     uint32_t base, chunk, off[KEEP ? kOps : 1];
     __device__ __forceinline__ uint32_t offset(uint32_t base, uint32_t chunk, int64_t ld, int D, int i) const {
         const uint32_t c = chunk ^ swizzle<DP>(i * kRows);
-        // columns past D lie past every range
-        return c * 8 < (uint32_t)D ? base + (uint32_t)(i * kRows * ld * 2) + c * 16 : 0x80000000u;
+        return c * 8 < (uint32_t)D ? base + (uint32_t)(i * kRows * ld * 2) + c * 16 : kNowhere;
     }
     __device__ __forceinline__ void init(int64_t ld, int D) {
         const int lane = threadIdx.x & 63, row = (threadIdx.x >> 6) * kOwnRows + lane / kChunks;

@@ -230,6 +230,7 @@ struct AttentionShape {
     int64_t ldq, ldk, ldv;      // row pitches, in elements
     float scale;
 };
+constexpr int64_t kMaxPitch = int64_t(1) << 23;  // of a row: the 128 rows of the largest tile lie within 2^31 bytes
 int64_t attention_groups(const AttentionShape &a);  // workgroups of the largest launch
 size_t attention_bwd_bytes(const AttentionShape &a);
 // cu: S + 1 starts on the device; o, res, dout dense [T x H x D] (res may be null); lse [H x T];

@@ -469,6 +469,12 @@ def _shaped(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> tor
     return t
 
 
+def _dense_workspace(ws: torch.Tensor) -> torch.Tensor:
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return ws
+
+
 def qlora_layernorm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                         eps: float = 1e-5, out: torch.Tensor | None = None, save_stats: bool = True):
     """y = (x - mean) rstd weight + bias over the rows of x [M, n] (bf16 or fp32, rows at any pitch).
@@ -512,8 +518,10 @@ def qlora_layernorm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
         dx = torch.empty_like(dy)
         dw = torch.empty(n, dtype=torch.float32, device=x.device) if need_dw else None
         db = torch.empty(n, dtype=torch.float32, device=x.device) if need_db else None
-    ws = workspace
-    if ws is None and (dw is not None or db is not None):
+    ws = None
+    if workspace is not None:
+        ws = _dense_workspace(workspace)
+    elif dw is not None or db is not None:
         ws = _workspace(layernorm_workspace_bytes(m, n), x.device)
     _check(_lib.qlora_layernorm_bwd(x.data_ptr(), dy.data_ptr(), kind, m, n, ld, mean.data_ptr(), rstd.data_ptr(),
                                     _ptr(weight), wkind, dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws),
@@ -601,7 +609,7 @@ def qlora_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: to
             if t.shape != like.shape:
                 raise ValueError(f"{name} must have shape {list(like.shape)}")
             pitches.append(_heads(t, rows, dim, name))
-    ws = workspace if workspace is not None else _workspace(
+    ws = _dense_workspace(workspace) if workspace is not None else _workspace(
         int(_lib.qlora_attention_workspace(ctypes.byref(shape))), q.device)
     _check(_lib.qlora_attention_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                     _ptr(residual), lse.data_ptr(), dout.data_ptr(), cu_seqlens.data_ptr(),
@@ -627,7 +635,7 @@ def qlora_logprob_fwd(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
     logp, entropy, lse = torch.empty(3, m, dtype=torch.float32, device=device).unbind(0)
     top_logp = torch.empty(m, top, dtype=torch.float32, device=device) if top > 0 else None
     top_ids = torch.empty_like(top_logp, dtype=torch.int32) if top > 0 else None
-    ws = workspace if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), device)
+    ws = _dense_workspace(workspace) if workspace is not None else _workspace(logprob_workspace_bytes(m, v, top), device)
     _check(_lib.qlora_logprob_fwd(logits.data_ptr(), kind, m, v, ld, targets.data_ptr(), int(top), logp.data_ptr(),
                                   entropy.data_ptr(), lse.data_ptr(), _ptr(top_logp), _ptr(top_ids), ws.data_ptr(),
                                   ws.numel(), _stream()), "qlora_logprob_fwd")

@@ -85,15 +85,22 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int64_t cnt, const U8x8 
         if (i < cnt) p[i] = (uint8_t)(r.w[i >> 2] >> (8 * (i & 3)));
 }
 
-constexpr int kLost = -128;  // m's code of an element whose states are not finite
-
+// Whether a byte of w is -128, m's code of an element whose states are not finite.
+__device__ __forceinline__ bool has_lost(uint32_t w) {
+    const uint32_t y = w ^ 0x80808080u;
+    return ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
+}
 __device__ __forceinline__ void decode(const U8x8 &mc, const U8x8 &vc, float m_scale, float v_scale, F8 &m, F8 &v) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int code = (int8_t)(mc.w[i >> 2] >> (8 * (i & 3)));
-        const float c = (float)code, d = (float)(uint8_t)(vc.w[i >> 2] >> (8 * (i & 3)));
-        m.v[i] = code == kLost ? NAN : c * fabsf(c) * m_scale;
-        v.v[i] = code == kLost ? NAN : d * d * (d * d) * v_scale;
+        const float c = (float)(int8_t)(mc.w[i >> 2] >> (8 * (i & 3))), d = (float)(uint8_t)(vc.w[i >> 2] >> (8 * (i & 3)));
+        m.v[i] = c * fabsf(c) * m_scale;
+        v.v[i] = d * d * (d * d) * v_scale;
+    }
+    if (has_lost(mc.w[0]) || has_lost(mc.w[1])) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((mc.w[i >> 2] >> (8 * (i & 3)) & 0xFFu) == 0x80u) m.v[i] = v.v[i] = NAN;
     }
 }
 
@@ -190,13 +197,21 @@ __device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyp
         store8((float *)t.v + at, FULL ? 8 : cnt, v);
         return;
     }
-    float mtop = 0.0f, vtop = 0.0f;
+    float z = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (!(fabsf(m.v[i]) < INFINITY && v.v[i] < INFINITY)) {
+    for (int i = 0; i < 8; ++i) z = fmaf(m.v[i], 0.0f, fmaf(v.v[i], 0.0f, z));
+    const bool lost = z != z;  // one of them
+    if (lost) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (fabsf(m.v[i]) < INFINITY && v.v[i] < INFINITY) continue;
             m.v[i] = NAN;  // which fmaxf leaves out
             v.v[i] = 0.0f;
         }
+    }
+    float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
         mtop = fmaxf(mtop, fabsf(m.v[i]));
         vtop = fmaxf(vtop, v.v[i]);
     }
@@ -220,11 +235,16 @@ __device__ __forceinline__ void adamw_group(const AdamwTensor &t, const AdamwHyp
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         int c = (int)fminf(cm[i], 127.0f);
-        c = m.v[i] < 0.0f ? -c : m.v[i] != m.v[i] ? kLost : c;
+        c = m.v[i] < 0.0f ? -c : c;
         mc.w[i >> 2] |= (uint32_t)(uint8_t)c << (8 * (i & 3));
         int d = (int)fminf(cv[i], 255.0f);
         if (v.v[i] > 0.0f && vs > 0.0f && d < 1) d = 1;
         vc.w[i >> 2] |= (uint32_t)d << (8 * (i & 3));
+    }
+    if (lost) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m.v[i] != m.v[i]) mc.w[i >> 2] ^= 0xFFu << (8 * (i & 3));  // 127, as fminf takes NaN, to -128
     }
     store_codes((uint8_t *)t.m + at, FULL ? 8 : cnt, mc);
     store_codes((uint8_t *)t.v + at, FULL ? 8 : cnt, vc);

@@ -12,10 +12,10 @@
 // Bound: the matrix cores from a few hundred rows on (4 D operations a pair and
 // head forward, 14 D backward: s and dp are formed twice so that every sum has
 // one owner and a fixed order, no atomics), HBM below.  Measured at D = 128: one
-// sequence of 8192 rows, H / Hk = 32 / 8, forward 517 us (1.06 PFLOP/s; the matrix cores busy
-// 55 % of the time, the exponentials and conversions between the products and the
-// LDS reads beside them); 4 x 1024, 32 / 32, forward 57 to 68 us, dq 80 to 93, dk and dv
-// 88 to 105 (0.55 to 0.8 PFLOP/s).
+// sequence of 8192 rows, H / Hk = 32 / 8, forward 507 to 530 us a call (1.04 to 1.08 PFLOP/s),
+// 537 to 591 in a trace of 20 (the matrix cores busy 54 % of the time, the exponentials and
+// conversions between the products and the LDS reads beside them); 4 x 1024, 32 / 32, forward
+// 59 to 68 us, dq 79 to 92, dk and dv 92 to 107 (0.5 to 0.7 PFLOP/s; least and median of 20).
 //
 // All products are 32 x 32 x 16 with the score tile transposed so that its
 // result layout is the next product's operand: the lane that receives score
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(64 * PARTS * GROUPS, 2) void attention_fwd_kernel(A
     __shared__ float meet[2][PARTS > 1 ? 64 * PARTS * GROUPS : 1];
     __shared__ int odd;  // a result is not finite
     const int head = head_of(blockIdx.x % a.H, a.H, a.Hk), kv = head / (a.H / a.Hk);
-    // the long rows' tiles first
+    // from the last rows back: of one sequence, those with the most keys first
     const Place at = place_of<OWN>(cu, a.S, a.T, slots - 1 - (int)(blockIdx.x / a.H));
     if (at.first >= at.end) return;
     const int64_t ldo = (int64_t)a.H * a.D;
@@ -748,7 +748,7 @@ __device__ __forceinline__ void store_rows_f32(float *y, int64_t ld, int row0, i
         }
 }
 
-// dk and dv of 128 keys: all rows after them, of one head (SPLIT: a workgroup a
+// dk and dv of OWN keys: all rows from them on, of one head (SPLIT: a workgroup a
 // head, partial results) or of all heads of the group.  The keys stay in LDS and
 // the values in registers: with both in registers the two accumulators leave no
 // room for two waves a SIMD.

@@ -188,7 +188,7 @@ hipError_t launch_layernorm_bwd(const void *x, const void *dy, bool x_f32, int64
 // ---- token log-probabilities (logprob.hip) --------------------------------------
 constexpr int kMaxTop = 16;                      // alternatives a row
 constexpr int64_t kMaxVocab = int64_t(1) << 19;  // 64 chunks of 8192: a lane each in the joining wave
-// A row's partial sums and best lists, and the workgroups the calls take.
+// The rows' partial sums, their groups' maxima, and the workgroups the calls take.
 size_t logprob_stats_bytes(int64_t M, int64_t V);
 size_t logprob_best_bytes(int64_t M, int64_t V, int top);
 int64_t logprob_groups(int64_t M, int64_t V);

@@ -23,7 +23,7 @@
 // orders, so the same bits on every run.  For rows wider than kMaxHeld a kernel
 // of its own reads x and dy by columns (4096 x 6144: 43 us in one pass, 64 in two).
 //
-// Measured: 4096 x 8192 bf16 with dw and db 36.4 + 4.9 us for 201 MB (5.5 TB/s in
+// Measured: 4096 x 8192 bf16 with dw and db 37 + 4.9 us for 201 MB (5.4 TB/s in
 // the main kernel; a copy reaches 5.2); 1531 x 2753 fp32 dx alone 11.2 us for 51 MB; one row
 // of 4096 forward 2.4 us.
 #include "elem8.hpp"

@@ -3,7 +3,7 @@
 //   H = -sum_v p_v log p_v = log l - (sum_v e^d_v d_v) / l,  d = x - max x, l = sum e^d
 //   the `top` largest x, equal ones in ascending order of index
 //   dx_v = g (delta_vt - p_v) - h p_v (log p_v + H)      g, h the gradients of logp and H
-// A logit of -inf is a forbidden token: p = 0, no part in H, gradient 0.  A row
+// A logit of -inf is a forbidden token: p = 0, no part in H, gradient 0 (g if it is the target).  A row
 // of -inf only has lse = -inf, logp = -inf, H = 0 and gradient 0.  A NaN or +inf
 // makes its row's results NaN.  A target outside [0, V) is no target: logp = 0 and
 // g is not used.

@@ -464,7 +464,8 @@ size_t qlora_attention_workspace(const qlora_attention_shape *shape);
  *   ds_ij = scale p (do_i v_j - do_i o_i)    dq_i = sum_j ds_ij k_j
  *   dk_j = sum_i ds_ij q_i                   dv_j = sum_i p do_i    (i over all heads of the group)
  *   o, residual (or NULL), lse  the forward's outputs;  dout  like o
- *   dq, dk, dv  device bf16, rows lddq, lddk, lddv elements apart (multiples of 8), written
+ *   dq, dk, dv  device bf16, rows lddq, lddk, lddv elements apart (multiples of 8), written;
+ *          apart from the inputs
  *   ws  >= qlora_attention_workspace(shape) bytes.
  */
 int qlora_attention_bwd(const qlora_attention_shape *shape, const qlora_bf16 *q, const qlora_bf16 *k,
@@ -495,7 +496,7 @@ size_t qlora_logprob_workspace(int64_t M, int64_t V, int32_t top);
  * indices.  A NaN or +inf in a row makes its results NaN (logp without a target
  * stays 0); the alternatives' indices never name a NaN: -1 where no other logit is left.
  * Errors: QLORA_EINVAL (null pointer, size <= 0, ld < V, top > V), QLORA_ENOTSUP
- * (unknown type, V > 2^19, top > 16, too many rows for one launch), QLORA_EALIGN,
+ * (unknown type, V > 2^19, top > 16, M ceil(V / 8192) >= 2^31), QLORA_EALIGN,
  * QLORA_EWORKSPACE.
  */
 int qlora_logprob_fwd(const void *logits, int32_t type, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
@@ -505,7 +506,8 @@ int qlora_logprob_fwd(const void *logits, int32_t type, int64_t M, int64_t V, in
 /*
  * qlora_logprob_bwd -- the gradient of qlora_logprob_fwd's logp and entropy:
  *   dlogits[m][v] = dlogp[m] ((v == targets[m]) - p) - dentropy[m] p (log p + entropy[m])
- * rounded once to `type`.  Ruled-out tokens and rows get 0.
+ * rounded once to `type`.  Rows that are ruled out throughout get 0, ruled-out tokens
+ * too (a ruled-out target its dlogp, by the formula).
  *   lse, entropy  the forward's outputs (entropy only with dentropy)
  *   dlogp (with targets), dentropy  device fp32 [M]; either may be NULL, not both
  *   dlogits device [M x V] of `type`, rows ldd >= V elements apart, written; may be

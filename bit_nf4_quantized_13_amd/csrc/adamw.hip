@@ -21,7 +21,7 @@
 // accesses), a block of 256 is half a wave, its maxima 5 lane exchanges.
 // Tensors go to the kernel as arguments, up to kMaxAdamwTensors a launch: nothing
 // about them is kept anywhere between calls.  Measured: 20 M elements in 56 tensors,
-// 8-bit states, 44 us (12.06 bytes each: 5.5 TB/s), their moments 34 us (10.06 bytes each);
+// 8-bit states, 45 us (12.06 bytes each: 5.4 TB/s), their moments 34 us (10.06 bytes each);
 // 65,536 elements with fp32 states 3.6 us.
 #include "elem8.hpp"
 #include "launch.hpp"
